@@ -349,6 +349,161 @@ DSA_API int dsa_decode(const void* q_idx, const void* k_idx, const void* w, cons
                        size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * (6b) RMS norm of every query and key head and the position rotation, in one pass over Q
+ * and K: what turns a layer's projections into the Q and K (or q_idx and k_idx) of the
+ * calls above.  The report summary does not describe this part of the decoder; these are
+ * the usual definitions.  Per row x = Q[t,h,:] (or K[t,h,:]) with weight g:
+ *     n = x / sqrt(mean(x^2) + eps) * g                    (weight NULL: n = x)
+ *     (u, v) -> (u cos a - v sin a, v cos a + u sin a),  a = position(t) * inv_freq[i]
+ * for i < rotary_dim/2 on the pairs (n[i], n[i + rotary_dim/2]), or with interleaved != 0
+ * on (n[2i], n[2i+1]); dims from rotary_dim on pass through.  All arithmetic is fp32 (the
+ * angle is reduced in fp64, so far positions lose nothing), rounded once to bf16.
+ *   Q device bf16 [total_q, Hq, d], K device bf16 [total_q, Hk, d] or NULL with Hk = 0;
+ *   q_stride, k_stride, ...: elements from one token to the next (>= heads * d, a multiple
+ *     of 8), so Q and K may be slices of one fused projection; heads are dense.
+ *   q_weight, k_weight device bf16 [d], each may be NULL;  inv_freq device fp64
+ *     [rotary_dim/2], radians per position, or NULL with rotary_dim = 0 (no rotation).
+ *   positions device int32 [total_q] or NULL.  NULL: the position of token i of sequence b
+ *     is i + seqlens_k[b] - Lq (seqlens_k device int32 [batch]: lengths with these tokens
+ *     included), or i where seqlens_k is NULL.  cu_seqlens_q NULL (then batch is 1 and
+ *     seqlens_k NULL): one sequence of total_q tokens.
+ *   Rows of tokens outside [cu_seqlens_q[0], cu_seqlens_q[batch]) are left untouched.
+ *   Q_out, K_out may be Q, K themselves (same stride); no other overlap is allowed.
+ * Supported: d in {32, 64, 128}; rotary_dim a multiple of 16; total_q * heads < 2^31.
+ * ------------------------------------------------------------------------------- */
+DSA_API int dsa_norm_rope(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                          const void* q_weight, const void* k_weight, float eps,
+                          const double* inv_freq, int rotary_dim, int interleaved,
+                          const int32_t* positions, const int32_t* cu_seqlens_q,
+                          const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk,
+                          int d, void* Q_out, int64_t q_out_stride, void* K_out,
+                          int64_t k_out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (6c) Gradient of (6b).  dQ_out, dK_out are the gradients at its outputs; Q, K its inputs.
+ *   dQ, dK device bf16, written for the same rows that (6b) writes; they may be dQ_out,
+ *     dK_out themselves (same stride).
+ *   dq_weight, dk_weight device fp32 [d]: the weights' gradients, summed over those tokens
+ *     and all heads (overwritten, not added to); each is required exactly where its weight
+ *     is not NULL.  The sums are taken in a fixed order: repeats are bit-identical.
+ *   workspace: dsa_norm_rope_bwd_workspace_size() bytes, 16-byte aligned (not read where
+ *     neither weight is given).
+ * ------------------------------------------------------------------------------- */
+DSA_API size_t dsa_norm_rope_bwd_workspace_size(int64_t total_q, int Hq, int Hk, int d);
+DSA_API int dsa_norm_rope_bwd(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                              const void* dQ_out, int64_t dq_out_stride, const void* dK_out,
+                              int64_t dk_out_stride, const void* q_weight, const void* k_weight,
+                              float eps, const double* inv_freq, int rotary_dim, int interleaved,
+                              const int32_t* positions, const int32_t* cu_seqlens_q,
+                              const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk,
+                              int d, void* dQ, int64_t dq_stride, void* dK, int64_t dk_stride,
+                              float* dq_weight, float* dk_weight, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * The paged cache of (7) to (7d).  A pool of num_pages pages of page_size positions each:
+ *   k_cache, v_cache device bf16 [num_pages, page_size, Hkv, d], k_idx_cache device bf16
+ *     [num_pages, page_size, d_I]; *_page_stride: elements from one page to the next (at
+ *     least a page, a multiple of 8), so one allocation may hold several caches by turns.
+ *   block_table device int32 [batch, max_pages]: position s of sequence b is row
+ *     s % page_size of page block_table[b, s / page_size].  Sequences may share pages.
+ *   seqlens_k device int32 [batch]: cached positions of each sequence, the new tokens
+ *     included.  It is read on the device only; a length past max_pages * page_size (or
+ *     past max_seqlen_k, where a call takes it) is cut there, a negative one counts as 0.
+ * A table entry outside [0, num_pages) is a page that is not there: nothing is written to it
+ * and its positions score -inf and are ignored by attention.  Entries past a sequence's
+ * length are not used.
+ * Supported: page_size a power of two from 16 to 1024; num_pages * page_size < 2^31.
+ *
+ * (7) Appends new tokens: K normed and rotated as in (6b), V as it is and k_idx (one head)
+ * normed and rotated with its own weight and frequencies, all in one launch.  Token i of
+ * sequence b (packed rows, cu_seqlens_q as everywhere) is written at position
+ * p = seqlens_k[b] - Lq + i; a token with p < 0, with p past the table or on a page that is
+ * not there writes nothing, and so do rows outside the sequences.  The rotation uses
+ * positions[t] where positions is not NULL, else p.  k_idx may be NULL with d_I = 0 (then
+ * k_idx_cache is not used).  Two tokens must not map to the same position of the same page.
+ * ------------------------------------------------------------------------------- */
+DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int64_t v_stride,
+                             const void* k_idx, int64_t k_idx_stride, const void* k_weight,
+                             const void* k_idx_weight, float eps, const double* inv_freq,
+                             int rotary_dim, int interleaved, const double* idx_inv_freq,
+                             int idx_rotary_dim, int idx_interleaved, const int32_t* positions,
+                             const int32_t* cu_seqlens_q, int64_t total_q, int Hkv, int d, int d_I,
+                             void* k_cache, int64_t k_page_stride, void* v_cache,
+                             int64_t v_page_stride, void* k_idx_cache, int64_t k_idx_page_stride,
+                             const int32_t* block_table, int max_pages, const int32_t* seqlens_k,
+                             int batch, int num_pages, int page_size, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (7a) Indexer scores over the paged cache: (1) with one query row per sequence, which sees
+ * its whole cache.  scores device fp32 [batch, ld_scores]: column s < the sequence's length
+ * receives position s's score, -inf on a page that is not there; the rest is untouched.
+ * (Several query rows of one sequence, as when drafted tokens are checked, are entries of
+ * their own with the same table row and growing lengths.)
+ * Supported: the (H_I, d_I) of (1).
+ * ------------------------------------------------------------------------------- */
+DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t k_idx_page_stride,
+                            const void* w, const int32_t* block_table, int max_pages,
+                            const int32_t* seqlens_k, int batch, int num_pages, int page_size,
+                            int max_seqlen_k, int H_I, int d_I, float* scores, int64_t ld_scores,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (7b) Decode attention over the paged cache: (4) with its positions looked up in the
+ * table.  Entries of indices outside [0, length) or on a page that is not there are ignored;
+ * an empty set gives O = 0 and lse = -inf.  One launch and no workspace.  Two equal entries
+ * of a row count twice, as in (3).
+ * Supported: the shapes of (4).
+ * ------------------------------------------------------------------------------- */
+DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int64_t k_page_stride,
+                                         const void* v_cache, int64_t v_page_stride,
+                                         const int32_t* indices, const int32_t* block_table,
+                                         int max_pages, const int32_t* seqlens_k, int batch,
+                                         int num_pages, int page_size, int Hq, int Hkv, int d,
+                                         int k, float scale, void* O, float* lse, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (7c) Whole DSA decode step over the paged cache: (7a), (2), then (7b), on a cache that
+ * holds the current token already.  indices device int32 [batch, k] receives the sets.
+ *   workspace: dsa_decode_paged_workspace_size(batch, max_seqlen_k) bytes.
+ * Supported: the shapes of (7a) and (7b); batch * max_seqlen_k < 2^31.
+ * ------------------------------------------------------------------------------- */
+DSA_API size_t dsa_decode_paged_workspace_size(int batch, int max_seqlen_k);
+DSA_API int dsa_decode_paged(const void* q_idx, const void* w, const void* Q, const void* k_cache,
+                             int64_t k_page_stride, const void* v_cache, int64_t v_page_stride,
+                             const void* k_idx_cache, int64_t k_idx_page_stride,
+                             const int32_t* block_table, int max_pages, const int32_t* seqlens_k,
+                             int batch, int num_pages, int page_size, int max_seqlen_k, int Hq,
+                             int Hkv, int d, int H_I, int d_I, int k, float scale, int32_t* indices,
+                             void* O, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * (7d) Whole DSA decode step from the projections of one new token per sequence: Q and
+ * q_idx normed and rotated (6b), K, V and k_idx appended (7), in one launch; then (7c).
+ * Row b of Q, K, V, q_idx, k_idx and w belongs to sequence b, whose new token sits at
+ * position seqlens_k[b] - 1 (rotated at positions[b] where positions is not NULL).
+ *   workspace: dsa_decode_step_paged_workspace_size() bytes.
+ * ------------------------------------------------------------------------------- */
+DSA_API size_t dsa_decode_step_paged_workspace_size(int batch, int max_seqlen_k, int Hq, int d,
+                                                    int H_I, int d_I);
+DSA_API int dsa_decode_step_paged(const void* q_idx, int64_t q_idx_stride, const void* w,
+                                  const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                                  const void* V, int64_t v_stride, const void* k_idx,
+                                  int64_t k_idx_stride, const void* q_weight, const void* k_weight,
+                                  const void* q_idx_weight, const void* k_idx_weight, float eps,
+                                  const double* inv_freq, int rotary_dim, int interleaved,
+                                  const double* idx_inv_freq, int idx_rotary_dim,
+                                  int idx_interleaved, const int32_t* positions, void* k_cache,
+                                  int64_t k_page_stride, void* v_cache, int64_t v_page_stride,
+                                  void* k_idx_cache, int64_t k_idx_page_stride,
+                                  const int32_t* block_table, int max_pages,
+                                  const int32_t* seqlens_k, int batch, int num_pages,
+                                  int page_size, int max_seqlen_k, int Hq, int Hkv, int d, int H_I,
+                                  int d_I, int k, float scale, int32_t* indices, void* O, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------
  * (7) Sparse attention backward.  Source: report summary section 1, sparse-adaptation
  * stage (the whole model trains through sparse attention); QbitAI launch article
  * (news.chathome.org): varlen DSA training kernels.  For the fixed sets in `indices` and

@@ -48,6 +48,29 @@ SIGNATURES = {
     "dsa_decode_workspace_size": (c_size, [c_int, c_int, c_int, c_int, c_int]),
     "dsa_decode": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64, c_int, c_int, c_int, c_int,
                            c_int, c_int, c_int, c_f32, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "dsa_norm_rope": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_f32, c_vp, c_int, c_int, c_vp, c_vp, c_vp,
+                              c_int, c_i64, c_int, c_int, c_int, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "dsa_norm_rope_bwd_workspace_size": (c_size, [c_i64, c_int, c_int, c_int]),
+    "dsa_norm_rope_bwd": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_f32, c_vp, c_int,
+                                  c_int, c_vp, c_vp, c_vp, c_int, c_i64, c_int, c_int, c_int, c_vp, c_i64, c_vp,
+                                  c_i64, c_vp, c_vp, c_vp, c_size, c_vp]),
+    "dsa_cache_append": (c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_f32, c_vp, c_int, c_int, c_vp,
+                                 c_int, c_int, c_vp, c_vp, c_i64, c_int, c_int, c_int, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                 c_i64, c_vp, c_int, c_vp, c_int, c_int, c_int, c_vp]),
+    "dsa_index_paged": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_int, c_vp, c_int, c_int, c_int, c_int, c_int, c_int,
+                                c_vp, c_i64, c_vp]),
+    "dsa_sparse_attn_decode_paged": (c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_int, c_vp, c_int, c_int,
+                                             c_int, c_int, c_int, c_int, c_int, c_f32, c_vp, c_vp, c_vp]),
+    "dsa_decode_paged_workspace_size": (c_size, [c_int, c_int]),
+    "dsa_decode_paged": (c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_int, c_vp, c_int,
+                                 c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_f32, c_vp, c_vp,
+                                 c_vp, c_vp, c_size, c_vp]),
+    "dsa_decode_step_paged_workspace_size": (c_size, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "dsa_decode_step_paged": (c_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp,
+                                      c_vp, c_vp, c_vp, c_f32, c_vp, c_int, c_int, c_vp, c_int, c_int, c_vp, c_vp,
+                                      c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_int, c_vp, c_int, c_int, c_int, c_int,
+                                      c_int, c_int, c_int, c_int, c_int, c_int, c_f32, c_vp, c_vp, c_vp, c_vp, c_size,
+                                      c_vp]),
     "dsa_sparse_attn_bwd_workspace_size": (c_size, [c_i64, c_i64, c_int, c_int, c_int, c_int]),
     "dsa_sparse_attn_prefill_bwd": (c_int, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_i64,
                                             c_i64, c_int, c_int, c_int, c_int, c_int, c_f32, c_vp, c_vp, c_vp,

@@ -470,7 +470,7 @@ int make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_
                       uint64_t row_pitch_bytes, uint32_t box_rows, uint32_t box_cols, int swizzle_bytes);
 
 int make_tmap_bf16_3d(CUtensorMap* map, const void* base, const uint64_t dims[3], const uint64_t strides[2],
-                      const uint32_t box[3]);
+                      const uint32_t box[3], int swizzle_bytes = 128);
 
 // The union form of the masked tensor-core attention passes (adjacent-query reuse): per
 // 16-row block the sorted union of its rows' selected positions, its size, the

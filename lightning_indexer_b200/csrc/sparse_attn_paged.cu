@@ -1,0 +1,331 @@
+// Attention of one query row per sequence over its selected positions in a paged key and
+// value cache (sm_100a).
+//
+//   O[b, h, :] = sum_{s in S_b} softmax_s(scale * Q[b, h, :] . K[s, g, :]) V[s, g, :],  g = h / (Hq / Hkv)
+//
+// S_b: the entries of indices[b, :] inside [0, len_b) whose page lies in the pool; position s
+// is row s mod P of page table[b, s / P].  An empty set gives O = 0 and lse = -inf.
+//
+// The work is a gather of 2 Hkv d bf16 per selected position; the products are 16 operations
+// per byte, so warp-level MMA carries them (16 keys x 8 heads, no padding) as in the gather
+// kernel of the contiguous cache.  One launch and no scratch memory: the selected slots of a
+// (row, KV head) are dealt in chunks of 16 to the warps of a thread-block cluster, each warp
+// runs one online softmax over its chunks, and the partial (max, sum, O) of the warps are
+// joined in shared memory, then over the cluster through distributed shared memory, always in
+// the same order.
+#include <algorithm>
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "warp_mma.cuh"
+
+namespace dsa {
+
+struct SAPagedParams {
+  const uint16_t* Q;  // [rows, Hq, D]
+  const uint16_t* K;  // [pages, P, Hkv, D], page strides below (elements)
+  const uint16_t* V;
+  long long k_page_stride, v_page_stride;
+  const int* indices;  // [rows, k]
+  const int* table;    // [rows, table_width]
+  const int* lens;     // [rows]
+  int table_width, page_shift, num_pages;
+  int Hq, Hkv, G, k;
+  float scale_log2;
+  uint16_t* O;  // [rows, Hq, D]
+  float* lse;   // [rows, Hq] or null
+};
+
+template <int D, int WARPS, int STAGES>
+struct SAPagedSmem {
+  static constexpr int STAGE_BYTES = 2 * 16 * D * 2;  // K and V rows of a chunk
+  static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
+  static constexpr int OFF_ML = RING;                    // [WARPS][8] float4: max, sum, rounded sum
+  static constexpr int OFF_CO = OFF_ML + WARPS * 8 * 16;  // [8][D] the block's O
+  static constexpr int OFF_CML = OFF_CO + 8 * D * 4;      // [8] float4
+  static constexpr int BYTES = OFF_CML + 8 * 16;
+  static_assert(STAGES * STAGE_BYTES >= 8 * D * 4, "a warp's O replaces its ring");
+};
+
+template <int D, int WARPS, int STAGES>
+__global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAPagedParams p, int splits) {
+  namespace cg = cooperative_groups;
+  using C = SAPagedSmem<D, WARPS, STAGES>;
+  constexpr int SEGS = D / 8, MT = D / 16;
+  constexpr int TILE_BYTES = C::STAGE_BYTES / 2;
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint8_t* my = smem + warp * STAGES * C::STAGE_BYTES;
+  const uint32_t my_s = smem_u32(my);
+  const int rank = blockIdx.x % splits, cid = blockIdx.x / splits;
+  const int g = cid % p.Hkv;
+  const long long row = cid / p.Hkv;
+
+  const int len = __ldg(p.lens + row);
+  const int* idx = p.indices + row * p.k;
+  const int* trow = p.table + row * p.table_width;
+  const int nchunks = p.k / 16, step = splits * WARPS, c0 = rank * WARPS + warp;
+  const int kv_row = p.Hkv * D;
+  const uint16_t* Kg = p.K + g * D;
+  const uint16_t* Vg = p.V + g * D;
+
+  uint32_t qb[MT][2];
+  {
+    const int head = lane / 4;
+    const bool hv = head < p.G;
+    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.Q + ((size_t)row * p.Hq + g * p.G + (hv ? head : 0)) * D);
+#pragma unroll
+    for (int kk = 0; kk < MT; ++kk) {
+      qb[kk][0] = hv ? __ldg(qrow + kk * 8 + (lane % 4)) : 0u;
+      qb[kk][1] = hv ? __ldg(qrow + kk * 8 + 4 + (lane % 4)) : 0u;
+    }
+  }
+
+  // cache slot (page * P + row in page) of the position in this lane's slot of chunk c, or -1
+  const int slot = lane & 15;
+  auto position = [&](int c) { return c < nchunks ? __ldg(idx + c * 16 + slot) : -1; };
+  auto cache_slot = [&](int s) {
+    if ((unsigned)s >= (unsigned)max(len, 0)) return -1;
+    const int pg = s >> p.page_shift;
+    if (pg >= p.table_width) return -1;
+    const int page = __ldg(trow + pg);
+    if ((unsigned)page >= (unsigned)p.num_pages) return -1;
+    return (page << p.page_shift) | (s & ((1 << p.page_shift) - 1));
+  };
+  // starts the copies of a chunk whose slots the lanes hold; returns its mask of valid slots
+  auto issue = [&](int st, int mine) -> uint32_t {
+    const uint32_t kdst = my_s + st * C::STAGE_BYTES, vdst = kdst + TILE_BYTES;
+    const int sub = lane >> 3, c = lane & 7;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 4 * j + sub;
+      const int cs = __shfl_sync(0xffffffffu, mine, r);
+      const bool valid = cs >= 0;
+      const int page = cs >> p.page_shift;
+      const int in = (cs & ((1 << p.page_shift) - 1)) * kv_row + c * 8;
+      const uint16_t* ksrc = valid ? Kg + page * p.k_page_stride + in : Kg;
+      const uint16_t* vsrc = valid ? Vg + page * p.v_page_stride + in : Vg;
+      const uint32_t o = tile_off<D>(r, c);
+#pragma unroll
+      for (int h = 0; h < SEGS / 8; ++h) {
+        cp_async_16(kdst + o + h * 128, ksrc + h * 64, valid);
+        cp_async_16(vdst + o + h * 128, vsrc + h * 64, valid);
+      }
+    }
+    cp_async_commit();
+    return __ballot_sync(0xffffffffu, mine >= 0) & 0xFFFFu;
+  };
+
+  float acc[MT][4] = {};
+  float m0 = -INFINITY, m1 = -INFINITY;  // running max (log2 domain) of heads h0, h1
+  float l0 = 0.f, l1 = 0.f;              // this lane's share of the sums (for the lse)
+  float r0 = 0.f, r1 = 0.f;              // the same of the bf16-rounded weights that multiply V
+
+  uint32_t vmr[STAGES];  // valid masks of the chunks in flight, the next one to use first
+  int s_next = position(c0), cs_next = -1;  // positions one chunk ahead of the slots
+  cs_next = cache_slot(s_next);
+  s_next = position(c0 + step);
+#pragma unroll
+  for (int j = 0; j < STAGES - 1; ++j) {
+    const int cur = cs_next;
+    cs_next = cache_slot(s_next);
+    s_next = position(c0 + (j + 2) * step);
+    vmr[j] = c0 + j * step < nchunks ? issue(j, cur) : (cp_async_commit(), 0u);
+  }
+
+  int n = 0;
+#pragma unroll 1
+  for (int c = c0; c < nchunks; c += step, ++n) {
+    const int st = n % STAGES;
+    {
+      const int cn = c + (STAGES - 1) * step;
+      const int cur = cs_next;
+      cs_next = cache_slot(s_next);
+      s_next = position(cn + 2 * step);
+      vmr[STAGES - 1] = cn < nchunks ? issue((n + STAGES - 1) % STAGES, cur) : (cp_async_commit(), 0u);
+    }
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();
+    const uint32_t vm = vmr[0];
+#pragma unroll
+    for (int j = 0; j + 1 < STAGES; ++j) vmr[j] = vmr[j + 1];
+    if (vm != 0) {  // warp-uniform: chunks of unused slots are passed over
+      const uint32_t kt = my_s + st * C::STAGE_BYTES, vt = kt + TILE_BYTES;
+      // ---- S^T = K_chunk . Q^T, two interleaved accumulator chains
+      float sa[4] = {}, sb[4] = {};
+#pragma unroll
+      for (int kk = 0; kk < MT; kk += 2) {
+        uint32_t a0, a1, a2, a3, e0, e1, e2, e3;
+        ldmatrix_x4(kt + tile_off<D>(lane & 15, kk * 2 + (lane >> 4)), a0, a1, a2, a3);
+        ldmatrix_x4(kt + tile_off<D>(lane & 15, (kk + 1) * 2 + (lane >> 4)), e0, e1, e2, e3);
+        mma_bf16_16816(sa, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+        mma_bf16_16816(sb, e0, e1, e2, e3, qb[kk + 1][0], qb[kk + 1][1]);
+      }
+      // keys of this lane: lane/4 and lane/4 + 8; heads h0 = 2*(lane%4), h1 = h0 + 1
+      const bool v0 = (vm >> (lane >> 2)) & 1u, v1 = (vm >> ((lane >> 2) + 8)) & 1u;
+      const float x00 = v0 ? (sa[0] + sb[0]) * p.scale_log2 : -INFINITY;
+      const float x01 = v0 ? (sa[1] + sb[1]) * p.scale_log2 : -INFINITY;
+      const float x10 = v1 ? (sa[2] + sb[2]) * p.scale_log2 : -INFINITY;
+      const float x11 = v1 ? (sa[3] + sb[3]) * p.scale_log2 : -INFINITY;
+      float cm0 = fmaxf(x00, x10), cm1 = fmaxf(x01, x11);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        cm0 = fmaxf(cm0, __shfl_xor_sync(0xffffffffu, cm0, o));
+        cm1 = fmaxf(cm1, __shfl_xor_sync(0xffffffffu, cm1, o));
+      }
+      // the max moves only by more than 8: every weight stays below 2^8
+      const bool up0 = cm0 > m0 + 8.f, up1 = cm1 > m1 + 8.f;
+      if (__any_sync(0xffffffffu, up0 || up1)) {
+        const float al0 = up0 ? exp2f(m0 - cm0) : 1.f, al1 = up1 ? exp2f(m1 - cm1) : 1.f;
+        if (up0) m0 = cm0;
+        if (up1) m1 = cm1;
+        l0 *= al0;
+        l1 *= al1;
+        r0 *= al0;
+        r1 *= al1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          acc[mt][0] *= al0;
+          acc[mt][1] *= al1;
+          acc[mt][2] *= al0;
+          acc[mt][3] *= al1;
+        }
+      }
+      const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
+      const float p00 = exp2f(x00 - mu0), p01 = exp2f(x01 - mu1);
+      const float p10 = exp2f(x10 - mu0), p11 = exp2f(x11 - mu1);
+      l0 += p00 + p10;
+      l1 += p01 + p11;
+      // P is rounded to bf16 for the product; O is divided by the sum of the rounded weights
+      const uint32_t pk0 = pack_bf16x2(p00, p01), pk1 = pack_bf16x2(p10, p11);
+      r0 += __uint_as_float(pk0 << 16) + __uint_as_float(pk1 << 16);
+      r1 += __uint_as_float(pk0 & 0xFFFF0000u) + __uint_as_float(pk1 & 0xFFFF0000u);
+      // ---- O^T += V^T . P^T
+      const uint32_t pb0 = movmatrix_trans(pk0), pb1 = movmatrix_trans(pk1);
+      const int vrow = (lane & 7) + ((lane >> 4) << 3), vseg_off = (lane >> 3) & 1;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        uint32_t a0, a1, a2, a3;
+        ldmatrix_x4_trans(vt + tile_off<D>(vrow, mt * 2 + vseg_off), a0, a1, a2, a3);
+        mma_bf16_16816(acc[mt], a0, a1, a2, a3, pb0, pb1);
+      }
+    }
+    __syncwarp();  // stage st is refilled by the next iteration's copies
+  }
+  cp_async_wait<0>();
+  __syncwarp();
+
+  // ---- the warp's state: sums over its lanes, O^T into its ring as [8][D]
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    r0 += __shfl_xor_sync(0xffffffffu, r0, o);
+    r1 += __shfl_xor_sync(0xffffffffu, r1, o);
+  }
+  const int h0 = 2 * (lane % 4);
+  float4* s_ml = reinterpret_cast<float4*>(smem + C::OFF_ML);
+  if (lane < 4) {
+    s_ml[warp * 8 + h0] = make_float4(m0, l0, r0, 0.f);
+    s_ml[warp * 8 + h0 + 1] = make_float4(m1, l1, r1, 0.f);
+  }
+  float* wo = reinterpret_cast<float*>(my);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int d0 = mt * 16 + lane / 4;
+    wo[h0 * D + d0] = acc[mt][0];
+    wo[(h0 + 1) * D + d0] = acc[mt][1];
+    wo[h0 * D + d0 + 8] = acc[mt][2];
+    wo[(h0 + 1) * D + d0 + 8] = acc[mt][3];
+  }
+  __syncthreads();
+
+  // ---- the block's state
+  float* s_co = reinterpret_cast<float*>(smem + C::OFF_CO);
+  float4* s_cml = reinterpret_cast<float4*>(smem + C::OFF_CML);
+  for (int e = threadIdx.x; e < p.G * D; e += WARPS * 32) {
+    const int h = e / D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w * 8 + h].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+    float o = 0.f, L = 0.f, R = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float4 ml = s_ml[w * 8 + h];
+      const float f = exp2f(ml.x - mu);  // a warp without keys: 2^-inf = 0
+      L = fmaf(ml.y, f, L);
+      R = fmaf(ml.z, f, R);
+      o = fmaf(reinterpret_cast<const float*>(smem + w * STAGES * C::STAGE_BYTES)[e], f, o);
+    }
+    s_co[e] = o;
+    if (e % D == 0) s_cml[h] = make_float4(M, L, R, 0.f);
+  }
+
+  // ---- over the cluster: each block finishes a share of the (head, dim) outputs
+  cg::cluster_group cluster = cg::this_cluster();
+  if (splits > 1) cluster.sync(); else __syncthreads();
+  for (int e = rank * WARPS * 32 + threadIdx.x; e < p.G * D; e += splits * WARPS * 32) {
+    const int h = e / D;
+    float M = -INFINITY;
+    for (int q = 0; q < splits; ++q) M = fmaxf(M, (splits > 1 ? cluster.map_shared_rank(s_cml, q) : s_cml)[h].x);
+    const float mu = M == -INFINITY ? 0.f : M;
+    float o = 0.f, L = 0.f, R = 0.f;
+    for (int q = 0; q < splits; ++q) {
+      const float4 ml = (splits > 1 ? cluster.map_shared_rank(s_cml, q) : s_cml)[h];
+      const float f = exp2f(ml.x - mu);
+      L = fmaf(ml.y, f, L);
+      R = fmaf(ml.z, f, R);
+      o = fmaf((splits > 1 ? cluster.map_shared_rank(s_co, q) : s_co)[e], f, o);
+    }
+    const long long head = row * p.Hq + g * p.G + h;
+    p.O[head * D + e % D] = __bfloat16_as_ushort(__float2bfloat16_rn(R > 0.f ? o / R : 0.f));
+    if (p.lse && e % D == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  }
+  if (splits > 1) cluster.sync();  // the other blocks may still read this one's state
+}
+
+}  // namespace dsa
+
+namespace dsa_host {
+
+template <int D>
+static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, cudaStream_t stream) {
+  constexpr int WARPS = 4, STAGES = 2;
+  auto kern = dsa::sparse_attn_paged_kernel<D, WARPS, STAGES>;
+  const int smem = dsa::SAPagedSmem<D, WARPS, STAGES>::BYTES;
+  static DeviceFlag done;
+  if (!done) {
+    cudaError_t e_ = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e_ == cudaSuccess) e_ = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (e_ != cudaSuccess) return cuda_fail(e_);
+    done = true;
+  }
+  const long long groups = (long long)batch * p.Hkv;
+  int splits = std::min(8, std::max(1, p.k / (16 * WARPS)));
+  while (splits > 1 && groups * splits > 0x7FFFFFFFLL) --splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * splits));
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, splits); e != cudaSuccess) return cuda_fail(e);
+  return last_launch_status();
+}
+
+int sparse_attn_paged_launch(const dsa::SAPagedParams& p, int batch, int d, bool pdl, cudaStream_t stream) {
+  return d == 128 ? sa_paged_launch_d<128>(p, batch, pdl, stream) : sa_paged_launch_d<64>(p, batch, pdl, stream);
+}
+
+}  // namespace dsa_host
