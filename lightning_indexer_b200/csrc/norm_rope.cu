@@ -16,7 +16,11 @@
 //
 // Layout: D / 16 lanes hold one row, 16 elements each in two 16-byte pieces chosen so that
 // both members of a rotation pair sit in the same lane, so the only exchange between lanes
-// is the norm's sum (and, backward, its dot product).  A warp takes 512 / D rows at once.
+// is the norm's sum (and, backward, its dot product).  A warp takes 512 / D rows at once, a
+// group, and runs over consecutive groups: their rows stream through a private ring in shared
+// memory by asynchronous copies (no registers held while they fly), and the places of the
+// run's tokens (sequence, position, page) are looked up by its lanes side by side, one chain
+// of dependent loads per run instead of one per group.
 #include <algorithm>
 
 #include "common.cuh"
@@ -35,6 +39,9 @@ struct HeadSeg {
   int interleaved, paged;
   int block0;           // first block of this tensor's rows
   int groups;           // warp-sized groups of 512 / D rows
+  int iters;            // groups of a run (forward: of a warp), at most 32 tokens' worth
+  unsigned div_mul;     // row / heads = (row * div_mul) >> div_shift for rows < 2^31
+  int div_shift;
   float* dg_part;       // backward with norm: [blocks of this tensor][D]
 };
 
@@ -57,7 +64,7 @@ constexpr int NR_WARPS = 8;
 struct HeadRowsParams {
   HeadSeg seg[NR_MAX_SEGS];
   int nseg;
-  int iters;  // groups per warp
+  int warp_iters;  // backward: groups of a warp
   float eps;
   TokenMap tk;
 };
@@ -126,35 +133,40 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// What a lane holds of every row of its segment: two 8-element pieces at e0 and e1.
-template <int D>
+// What a lane holds of every row of its segment: two 8-element pieces at e0 and e1, each
+// instruction of the row's lanes covering whole 16-byte pieces side by side.
+template <int D, bool INTER>
 struct LaneCols {
   static constexpr int LPR = D / 16;       // lanes per row
   static constexpr int RPW = 32 / LPR;     // rows per warp
+  int sub;
   int e0, e1;
-  bool rot;  // this lane's pairs rotate (frequencies 8 sub .. 8 sub + 7)
+  bool rot0, rot1;  // whether the pairs 0-3 and 4-7 of this lane rotate
 
-  __device__ __forceinline__ LaneCols(const HeadSeg& s, int sub, bool inter) {
-    const int nrot = s.inv_freq ? s.rotary / 16 : 0;  // rotating lanes
-    rot = sub < nrot;
-    if (inter) {
-      e0 = 16 * sub;
-      e1 = e0 + 8;
-    } else if (rot) {
+  __device__ __forceinline__ LaneCols(const HeadSeg& s, int sub_) : sub(sub_) {
+    const int r16 = s.inv_freq ? s.rotary / 16 : 0;
+    if (INTER) {  // pairs lie inside a piece
       e0 = 8 * sub;
-      e1 = 8 * (sub + nrot);
-    } else {
-      e0 = 16 * sub;  // pieces 2 nrot + 2 (sub - nrot) and the next
-      e1 = e0 + 8;
+      e1 = e0 + D / 2;
+      rot0 = e0 < 16 * r16;
+      rot1 = e1 < 16 * r16;
+    } else {  // pair p is element p of the two pieces; the lanes past r16 share the dims that pass
+      rot0 = rot1 = sub < r16;
+      e0 = rot0 ? 8 * sub : 8 * (sub + r16);
+      e1 = rot0 ? 8 * (sub + r16) : 8 * (sub + LPR);
     }
+  }
+  __device__ __forceinline__ bool rotates(int p) const { return p < 4 ? rot0 : rot1; }
+  __device__ __forceinline__ int freq(int p) const {
+    return INTER ? (p < 4 ? 4 * sub + p : 4 * sub + D / 4 + p - 4) : 8 * sub + p;
   }
 };
 
 // cos and sin of this lane's eight pairs at its row's position.  Where every row of the warp
 // belongs to one token, each of the warp's row groups computes a share and they exchange.
-template <int D>
-__device__ __forceinline__ void lane_turns(const HeadSeg& s, bool shared, bool rot, int sub, int rg, int pos, float* c,
-                                           float* sn) {
+template <int D, bool INTER>
+__device__ __forceinline__ void lane_turns(const HeadSeg& s, const LaneCols<D, INTER>& col, bool shared, int rg, int pos,
+                                           float* c, float* sn) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;
   constexpr int PER = RPW >= 8 ? 1 : 8 / RPW;  // pairs per row group when shared
   if (shared) {
@@ -162,20 +174,20 @@ __device__ __forceinline__ void lane_turns(const HeadSeg& s, bool shared, bool r
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int p = (rg * PER + j) & 7;
-      if (rot) turn(s.inv_freq[8 * sub + p], pos, mc[j], ms[j]);
-      else mc[j] = 1.f, ms[j] = 0.f;
+      mc[j] = 1.f, ms[j] = 0.f;
+      if (col.rotates(p)) turn(s.inv_freq[col.freq(p)], pos, mc[j], ms[j]);
     }
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      const int src = (p / PER) * LPR + sub;
+      const int src = (p / PER) * LPR + col.sub;
       c[p] = __shfl_sync(0xffffffffu, mc[p % PER], src);
       sn[p] = __shfl_sync(0xffffffffu, ms[p % PER], src);
     }
   } else {
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      if (rot) turn(s.inv_freq[8 * sub + p], pos, c[p], sn[p]);
-      else c[p] = 1.f, sn[p] = 0.f;
+      c[p] = 1.f, sn[p] = 0.f;
+      if (col.rotates(p)) turn(s.inv_freq[col.freq(p)], pos, c[p], sn[p]);
     }
   }
 }
@@ -189,73 +201,125 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // Pair rotation of the lane's 16 values (two pieces) by the angles (c, sgn * sn).
 template <bool INTER>
-__device__ __forceinline__ void rotate16(float* a, float* b, const float* c, const float* sn, float sgn) {
+__device__ __forceinline__ void rotate16(float* a, float* b, bool rot0, bool rot1, const float* c, const float* sn, float sgn) {
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    float& u = INTER ? (p < 4 ? a[2 * (p & 3)] : b[2 * (p & 3)]) : a[p];
-    float& v = INTER ? (p < 4 ? a[2 * (p & 3) + 1] : b[2 * (p & 3) + 1]) : b[p];
-    const float s = sgn * sn[p], u0 = u, v0 = v;
-    u = fmaf(u0, c[p], -(v0 * s));
-    v = fmaf(v0, c[p], u0 * s);
+  for (int half = 0; half < 2; ++half) {
+    if (!(half ? rot1 : rot0)) continue;  // dims that pass stay out of every product
+#pragma unroll
+    for (int p = 4 * half; p < 4 * half + 4; ++p) {
+      float& u = INTER ? (p < 4 ? a[2 * (p & 3)] : b[2 * (p & 3)]) : a[p];
+      float& v = INTER ? (p < 4 ? a[2 * (p & 3) + 1] : b[2 * (p & 3) + 1]) : b[p];
+      const float s = sgn * sn[p], u0 = u, v0 = v;
+      u = fmaf(u0, c[p], -(v0 * s));
+      v = fmaf(v0, c[p], u0 * s);
+    }
   }
 }
 
+__device__ __forceinline__ int row_token(const HeadSeg& s, unsigned r) {
+  return (int)(((unsigned long long)r * s.div_mul) >> s.div_shift);
+}
+
+// The places of the tokens t_first, t_first + 1, ..., one per lane, and their exchange.
+struct RunPlaces {
+  int pos;
+  bool ok;
+  long long yoff;
+  __device__ __forceinline__ void look_up(const TokenMap& tk, const HeadSeg& s, int t_first, int t_last, int lane) {
+    pos = 0;
+    yoff = 0;
+    ok = t_first + lane <= t_last && place_token(tk, s, t_first + lane, pos, yoff);
+  }
+  __device__ __forceinline__ void take(const RunPlaces& all, int i) {
+    pos = __shfl_sync(0xffffffffu, all.pos, i);
+    ok = __shfl_sync(0xffffffffu, (int)all.ok, i) != 0;
+    yoff = __shfl_sync(0xffffffffu, all.yoff, i);
+  }
+};
+
+constexpr int NR_FWD_STAGES = 4;  // groups in flight per warp
+constexpr int NR_GROUP_BYTES = 1024;
+
 template <int D, bool INTER>
-__device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane) {
-  using L = LaneCols<D>;
+__device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane,
+                                              uint8_t* ring) {
+  using L = LaneCols<D, INTER>;
+  constexpr int S = NR_FWD_STAGES;
   const int sub = lane % L::LPR, rg = lane / L::LPR;
-  const L col(s, sub, INTER);
+  const L col(s, sub);
   const unsigned H = s.heads;
   const bool shared = H % L::RPW == 0;
   const unsigned rows = (unsigned)p.tk.T * H;
-  float g0[8], g1[8];
+  const int grp0 = warp_in_seg * s.iters, n = min(s.iters, s.groups - grp0);
+  if (n <= 0) return;
+  const unsigned row0 = (unsigned)grp0 * L::RPW;
+  uint8_t* mine = ring + lane * 16;
+  auto issue = [&](int it) {
+    const unsigned r = row0 + it * L::RPW + rg;
+    if (it < n && r < rows) {
+      const int t = row_token(s, r);
+      const uint16_t* src = s.x + (long long)t * s.x_stride + (r - (unsigned)t * H) * D;
+      const uint32_t dst = smem_u32(mine + (it % S) * NR_GROUP_BYTES);
+      cp_async_16(dst, src + col.e0, true);
+      cp_async_16(dst + 512, src + col.e1, true);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  const int t_first = row_token(s, row0), t_last = row_token(s, min(row0 + n * L::RPW, rows) - 1);
+  RunPlaces all, cur;
+  all.look_up(p.tk, s, t_first, t_last, lane);
+  uint4 ga = {}, gb = {};
   if (s.g) {
-    unpack8(*reinterpret_cast<const uint4*>(s.g + col.e0), g0);
-    unpack8(*reinterpret_cast<const uint4*>(s.g + col.e1), g1);
+    ga = *reinterpret_cast<const uint4*>(s.g + col.e0);
+    gb = *reinterpret_cast<const uint4*>(s.g + col.e1);
   }
+  float g0[8], g1[8];
+  unpack8(ga, g0);
+  unpack8(gb, g1);
   float c[8], sn[8];
-  int cur = -1;
-  bool ok = false;
-  long long yoff = 0;
-  for (int it = 0; it < p.iters; ++it) {
-    const int grp = warp_in_seg * p.iters + it;
-    if (grp >= s.groups) break;  // warp-uniform
-    const unsigned r = (unsigned)grp * L::RPW + rg;
-    const int t = r < rows ? (int)(r / H) : p.tk.T;
+  int cur_t = -1;
+#pragma unroll 1
+  for (int it = 0; it < n; ++it) {
+    issue(it + S - 1);
+    const unsigned r = row0 + it * L::RPW + rg;
+    const int t = r < rows ? row_token(s, r) : t_last;
     const unsigned h = r - (unsigned)t * H;
-    uint4 xa = {}, xb = {};
-    if (r < rows) {
-      const uint16_t* src = s.x + (long long)t * s.x_stride + h * D;
-      xa = *reinterpret_cast<const uint4*>(src + col.e0);
-      xb = *reinterpret_cast<const uint4*>(src + col.e1);
+    if (__any_sync(0xffffffffu, t != cur_t)) {
+      cur_t = t;
+      cur.take(all, t - t_first);
+      if (s.inv_freq) lane_turns(s, col, shared, rg, cur.pos, c, sn);
     }
-    if (__any_sync(0xffffffffu, t != cur)) {
-      cur = t;
-      int pos = 0;
-      ok = place_token(p.tk, s, t, pos, yoff);
-      if (s.inv_freq) lane_turns<D>(s, shared, col.rot, sub, rg, pos, c, sn);
-    }
-    float a[8], b[8];
-    unpack8(xa, a);
-    unpack8(xb, b);
-    if (s.g) {
-      float ss = 0.f;
+    cp_async_wait<S - 1>();
+    uint4 xa = *reinterpret_cast<const uint4*>(mine + (it % S) * NR_GROUP_BYTES);
+    uint4 xb = *reinterpret_cast<const uint4*>(mine + (it % S) * NR_GROUP_BYTES + 512);
+    if (s.g || s.inv_freq) {  // else the rows pass as they are
+      float a[8], b[8];
+      unpack8(xa, a);
+      unpack8(xb, b);
+      if (s.g) {
+        float ss = 0.f, st = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-      const float rstd = rsqrtf(row_sum<L::LPR>(ss) * (1.f / D) + p.eps);
+        for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss), st = fmaf(b[i], b[i], st);
+        const float rstd = rsqrtf(row_sum<L::LPR>(ss + st) * (1.f / D) + p.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] *= rstd * g0[i];
-        b[i] *= rstd * g1[i];
+        for (int i = 0; i < 8; ++i) {
+          a[i] *= rstd * g0[i];
+          b[i] *= rstd * g1[i];
+        }
       }
+      rotate16<INTER>(a, b, col.rot0, col.rot1, c, sn, 1.f);
+      xa = pack8(a);
+      xb = pack8(b);
     }
-    if (s.inv_freq && col.rot) rotate16<INTER>(a, b, c, sn, 1.f);
-    if (ok) {
-      uint16_t* dst = s.y + yoff + h * D;
-      *reinterpret_cast<uint4*>(dst + col.e0) = pack8(a);
-      *reinterpret_cast<uint4*>(dst + col.e1) = pack8(b);
+    if (cur.ok && r < rows) {
+      uint16_t* dst = s.y + cur.yoff + h * D;
+      *reinterpret_cast<uint4*>(dst + col.e0) = xa;
+      *reinterpret_cast<uint4*>(dst + col.e1) = xb;
     }
   }
+  cp_async_wait<0>();
 }
 
 __device__ __forceinline__ int block_seg(const HeadRowsParams& p) {
@@ -266,96 +330,125 @@ __device__ __forceinline__ int block_seg(const HeadRowsParams& p) {
   return i;
 }
 
-__global__ void __launch_bounds__(NR_WARPS * 32) head_rows_fwd_kernel(const __grid_constant__ HeadRowsParams p) {
+__global__ void __launch_bounds__(NR_WARPS * 32, 3) head_rows_fwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
+  __shared__ __align__(16) uint8_t rings[NR_WARPS][NR_FWD_STAGES * NR_GROUP_BYTES];
   const HeadSeg& s = p.seg[block_seg(p)];
   const int w = ((int)blockIdx.x - s.block0) * NR_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint8_t* ring = rings[threadIdx.x / 32];
   if (s.interleaved) {
-    if (s.D == 128) head_rows_fwd<128, true>(p, s, w, lane);
-    else if (s.D == 64) head_rows_fwd<64, true>(p, s, w, lane);
-    else head_rows_fwd<32, true>(p, s, w, lane);
+    if (s.D == 128) head_rows_fwd<128, true>(p, s, w, lane, ring);
+    else if (s.D == 64) head_rows_fwd<64, true>(p, s, w, lane, ring);
+    else head_rows_fwd<32, true>(p, s, w, lane, ring);
   } else {
-    if (s.D == 128) head_rows_fwd<128, false>(p, s, w, lane);
-    else if (s.D == 64) head_rows_fwd<64, false>(p, s, w, lane);
-    else head_rows_fwd<32, false>(p, s, w, lane);
+    if (s.D == 128) head_rows_fwd<128, false>(p, s, w, lane, ring);
+    else if (s.D == 64) head_rows_fwd<64, false>(p, s, w, lane, ring);
+    else head_rows_fwd<32, false>(p, s, w, lane, ring);
   }
 }
 
+constexpr int NR_BWD_STAGES = 3;  // groups in flight per warp, of x and of dy
+
 template <int D, bool INTER>
 __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane,
-                                              float* acc_smem) {
-  using L = LaneCols<D>;
+                                              uint8_t* ring, float* acc_smem) {
+  using L = LaneCols<D, INTER>;
+  constexpr int S = NR_BWD_STAGES;
   const int sub = lane % L::LPR, rg = lane / L::LPR;
-  const L col(s, sub, INTER);
+  const L col(s, sub);
   const unsigned H = s.heads;
   const bool shared = H % L::RPW == 0;
   const unsigned rows = (unsigned)p.tk.T * H;
-  float g0[8], g1[8], dg0[8] = {}, dg1[8] = {};
-  if (s.g) {
-    unpack8(*reinterpret_cast<const uint4*>(s.g + col.e0), g0);
-    unpack8(*reinterpret_cast<const uint4*>(s.g + col.e1), g1);
-  }
-  float c[8], sn[8];
-  int cur = -1;
-  bool ok = false;
-  long long yoff = 0;
-  for (int it = 0; it < p.iters; ++it) {
-    const int grp = warp_in_seg * p.iters + it;
-    if (grp >= s.groups) break;  // warp-uniform
-    const unsigned r = (unsigned)grp * L::RPW + rg;
-    const int t = r < rows ? (int)(r / H) : p.tk.T;
-    const unsigned h = r - (unsigned)t * H;
-    uint4 xa = {}, xb = {}, ya = {}, yb = {};
-    if (r < rows) {
+  const int grp0 = (int)min((long long)warp_in_seg * p.warp_iters, (long long)s.groups);
+  const int n = min(p.warp_iters, s.groups - grp0);
+  const unsigned row0 = (unsigned)grp0 * L::RPW;
+  uint8_t* mine = ring + lane * 16;
+  auto issue = [&](int it) {
+    const unsigned r = row0 + it * L::RPW + rg;
+    if (it < n && r < rows) {
+      const int t = row_token(s, r);
+      const unsigned h = r - (unsigned)t * H;
+      const uint32_t dst = smem_u32(mine + (it % S) * 2 * NR_GROUP_BYTES);
       const uint16_t* src = s.dy + (long long)t * s.dy_stride + h * D;
-      ya = *reinterpret_cast<const uint4*>(src + col.e0);
-      yb = *reinterpret_cast<const uint4*>(src + col.e1);
+      cp_async_16(dst, src + col.e0, true);
+      cp_async_16(dst + 512, src + col.e1, true);
       if (s.g) {
         src = s.x + (long long)t * s.x_stride + h * D;
-        xa = *reinterpret_cast<const uint4*>(src + col.e0);
-        xb = *reinterpret_cast<const uint4*>(src + col.e1);
+        cp_async_16(dst + 1024, src + col.e0, true);
+        cp_async_16(dst + 1536, src + col.e1, true);
       }
     }
-    if (__any_sync(0xffffffffu, t != cur)) {
-      cur = t;
-      int pos = 0;
-      ok = place_token(p.tk, s, t, pos, yoff);
-      if (s.inv_freq) lane_turns<D>(s, shared, col.rot, sub, rg, pos, c, sn);
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(i);
+  uint4 ga = {}, gb = {};
+  if (s.g) {
+    ga = *reinterpret_cast<const uint4*>(s.g + col.e0);
+    gb = *reinterpret_cast<const uint4*>(s.g + col.e1);
+  }
+  float dg0[8] = {}, dg1[8] = {}, c[8], sn[8];
+  RunPlaces all, cur;
+  int cur_t = -1, t_first = 0, run_end = 0;
+#pragma unroll 1
+  for (int it = 0; it < n; ++it) {
+    if (it == run_end) {  // the next run's tokens
+      run_end = min(it + s.iters, n);
+      t_first = row_token(s, row0 + it * L::RPW);
+      all.look_up(p.tk, s, t_first, row_token(s, min(row0 + run_end * L::RPW, rows) - 1), lane);
     }
+    issue(it + S - 1);
+    const unsigned r = row0 + it * L::RPW + rg;
+    const bool in = r < rows;
+    const int t = in ? row_token(s, r) : t_first;
+    const unsigned h = r - (unsigned)t * H;
+    if (__any_sync(0xffffffffu, t != cur_t)) {
+      cur_t = t;
+      cur.take(all, t - t_first);
+      if (s.inv_freq) lane_turns(s, col, shared, rg, cur.pos, c, sn);
+    }
+    const bool ok = cur.ok && in;
+    cp_async_wait<S - 1>();
+    const uint4* st = reinterpret_cast<const uint4*>(mine + (it % S) * 2 * NR_GROUP_BYTES);
     float a[8], b[8];
-    unpack8(ya, a);
-    unpack8(yb, b);
-    if (s.inv_freq && col.rot) rotate16<INTER>(a, b, c, sn, -1.f);
+    unpack8(st[0], a);
+    unpack8(st[32], b);
+    rotate16<INTER>(a, b, col.rot0, col.rot1, c, sn, -1.f);
     if (s.g) {
-      float xf[8], xg[8];
-      unpack8(xa, xf);
-      unpack8(xb, xg);
+      float xf[8], xg[8], g[8];
+      unpack8(st[64], xf);
+      unpack8(st[96], xg);
       float ss = 0.f, dot = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ss = fmaf(xf[i], xf[i], fmaf(xg[i], xg[i], ss));
-        dot = fmaf(a[i] * g0[i], xf[i], fmaf(b[i] * g1[i], xg[i], dot));
-      }
+      for (int i = 0; i < 8; ++i) ss = fmaf(xf[i], xf[i], fmaf(xg[i], xg[i], ss));
       const float rstd = rsqrtf(row_sum<L::LPR>(ss) * (1.f / D) + p.eps);
-      const float mean = row_sum<L::LPR>(dot) * rstd * (1.f / D);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xf[i] *= rstd, xg[i] *= rstd;  // xh
+      if (ok) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dg0[i] = fmaf(a[i], xf[i], dg0[i]), dg1[i] = fmaf(b[i], xg[i], dg1[i]);
+      }
+      unpack8(ga, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] *= g[i], dot = fmaf(a[i], xf[i], dot);
+      unpack8(gb, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] *= g[i], dot = fmaf(b[i], xg[i], dot);
+      const float mean = row_sum<L::LPR>(dot) * (1.f / D);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float h0 = xf[i] * rstd, h1 = xg[i] * rstd;
-        if (ok) {
-          dg0[i] = fmaf(a[i], h0, dg0[i]);
-          dg1[i] = fmaf(b[i], h1, dg1[i]);
-        }
-        a[i] = rstd * (a[i] * g0[i] - h0 * mean);
-        b[i] = rstd * (b[i] * g1[i] - h1 * mean);
+        a[i] = rstd * fmaf(-xf[i], mean, a[i]);
+        b[i] = rstd * fmaf(-xg[i], mean, b[i]);
       }
     }
     if (ok) {
-      uint16_t* dst = s.y + yoff + h * D;
+      uint16_t* dst = s.y + cur.yoff + h * D;
       *reinterpret_cast<uint4*>(dst + col.e0) = pack8(a);
       *reinterpret_cast<uint4*>(dst + col.e1) = pack8(b);
     }
   }
+  cp_async_wait<0>();
   if (!s.g) return;  // block-uniform
   // the block's share of dg: rows of the warp, then the warps in order
 #pragma unroll
@@ -382,20 +475,27 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
   }
 }
 
-__global__ void __launch_bounds__(NR_WARPS * 32) head_rows_bwd_kernel(const __grid_constant__ HeadRowsParams p) {
+struct HeadRowsBwdSmem {
+  __align__(16) uint8_t rings[NR_WARPS][NR_BWD_STAGES * 2 * NR_GROUP_BYTES];
+  float acc[NR_WARPS * 128];
+};
+
+__global__ void __launch_bounds__(NR_WARPS * 32, 2) head_rows_bwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float acc[NR_WARPS * 128];
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  HeadRowsBwdSmem& sm = *reinterpret_cast<HeadRowsBwdSmem*>(smem_raw);
   const HeadSeg& s = p.seg[block_seg(p)];
   const int w = ((int)blockIdx.x - s.block0) * NR_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint8_t* ring = sm.rings[threadIdx.x / 32];
   if (s.interleaved) {
-    if (s.D == 128) head_rows_bwd<128, true>(p, s, w, lane, acc);
-    else if (s.D == 64) head_rows_bwd<64, true>(p, s, w, lane, acc);
-    else head_rows_bwd<32, true>(p, s, w, lane, acc);
+    if (s.D == 128) head_rows_bwd<128, true>(p, s, w, lane, ring, sm.acc);
+    else if (s.D == 64) head_rows_bwd<64, true>(p, s, w, lane, ring, sm.acc);
+    else head_rows_bwd<32, true>(p, s, w, lane, ring, sm.acc);
   } else {
-    if (s.D == 128) head_rows_bwd<128, false>(p, s, w, lane, acc);
-    else if (s.D == 64) head_rows_bwd<64, false>(p, s, w, lane, acc);
-    else head_rows_bwd<32, false>(p, s, w, lane, acc);
+    if (s.D == 128) head_rows_bwd<128, false>(p, s, w, lane, ring, sm.acc);
+    else if (s.D == 64) head_rows_bwd<64, false>(p, s, w, lane, ring, sm.acc);
+    else head_rows_bwd<32, false>(p, s, w, lane, ring, sm.acc);
   }
 }
 
@@ -407,7 +507,7 @@ struct DgParams {
   int blocks[2];
   int D;
 };
-__global__ void __launch_bounds__(256) head_rows_dg_kernel(const DgParams p) {
+__global__ void __launch_bounds__(256) head_rows_dg_kernel(const __grid_constant__ DgParams p) {
   pdl_wait();
   pdl_trigger();
   __shared__ float acc[32][8];
@@ -429,33 +529,36 @@ __global__ void __launch_bounds__(256) head_rows_dg_kernel(const DgParams p) {
 
 namespace dsa_host {
 
-static void head_seg_blocks(dsa::HeadRowsParams& p) {
-  int block = 0;
+static long long seg_groups(const dsa::HeadRowsParams& p, const dsa::HeadSeg& s) {
+  const long long rpw = 512 / s.D;
+  return ((long long)p.tk.T * s.heads + rpw - 1) / rpw;
+}
+// Fills in what the kernels read of each segment; a warp takes warp_iters groups, or where
+// that is 0 as many as make a run.  Returns the number of blocks.
+static int plan_segs(dsa::HeadRowsParams& p, int run, int warp_iters) {
+  long long block = 0;
   for (int i = 0; i < p.nseg; ++i) {
     dsa::HeadSeg& s = p.seg[i];
-    const long long rows = (long long)p.tk.T * s.heads, rpw = 512 / s.D;
-    s.groups = (int)((rows + rpw - 1) / rpw);
-    s.block0 = block;
-    const long long per_block = (long long)p.iters * dsa::NR_WARPS;
-    block += (int)((s.groups + per_block - 1) / per_block);
+    const int rpw = 512 / s.D;
+    s.groups = (int)seg_groups(p, s);
+    // consecutive rows touch at most rows / heads + 2 tokens (exactly rows where heads is 1)
+    s.iters = std::min(run, std::max(1, (s.heads == 1 ? 32 : 30 * s.heads) / rpw));
+    int lg = 0;
+    while ((1LL << lg) < s.heads) ++lg;
+    s.div_shift = 31 + lg;
+    s.div_mul = (unsigned)(((1ULL << (31 + lg)) + s.heads - 1) / s.heads);
+    s.block0 = (int)block;
+    const long long per_block = (long long)(warp_iters ? warp_iters : s.iters) * dsa::NR_WARPS;
+    block += (s.groups + per_block - 1) / per_block;
   }
-}
-static int head_rows_blocks(const dsa::HeadRowsParams& p) {
-  const dsa::HeadSeg& s = p.seg[p.nseg - 1];
-  const long long per_block = (long long)p.iters * dsa::NR_WARPS;
-  return s.block0 + (int)((s.groups + per_block - 1) / per_block);
-}
-static long long head_rows_groups(const dsa::HeadRowsParams& p) {
-  long long n = 0;
-  for (int i = 0; i < p.nseg; ++i) n += ((long long)p.tk.T * p.seg[i].heads + 512 / p.seg[i].D - 1) / (512 / p.seg[i].D);
-  return n;
+  return (int)block;
 }
 
 int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) {
-  p.iters = head_rows_groups(p) > 32LL * sm_count() ? 8 : 1;
-  head_seg_blocks(p);
-  return launch_pdl(pdl, dsa::head_rows_fwd_kernel, dim3((unsigned)head_rows_blocks(p)), dim3(dsa::NR_WARPS * 32), 0,
-                    stream, p);
+  long long groups = 0;
+  for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
+  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1, 0);
+  return launch_pdl(pdl, dsa::head_rows_fwd_kernel, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), 0, stream, p);
 }
 
 // Groups per warp of the backward: the whole call in at most 16 warps' worth per SM.
@@ -469,9 +572,10 @@ size_t norm_rope_bwd_ws_bytes(long long T, int Hq, int Hk, int d) {
   return (size_t)((nq + per_block - 1) / per_block + (nk + per_block - 1) / per_block) * d * sizeof(float);
 }
 int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], cudaStream_t stream) {
-  p.iters = bwd_iters(head_rows_groups(p));
-  head_seg_blocks(p);
-  const int blocks = head_rows_blocks(p);
+  long long groups = 0;
+  for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
+  p.warp_iters = bwd_iters(groups);
+  const int blocks = plan_segs(p, 8, p.warp_iters);
   dsa::DgParams q{};
   int n = 0;
   for (int i = 0; i < p.nseg; ++i) {
@@ -483,8 +587,16 @@ int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], 
     q.blocks[n++] = (i + 1 < p.nseg ? p.seg[i + 1].block0 : blocks) - s.block0;
     q.D = s.D;
   }
-  if (const int st = launch_pdl(false, dsa::head_rows_bwd_kernel, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), 0,
-                                stream, p);
+  static DeviceFlag attr_done;
+  if (!attr_done) {
+    if (const cudaError_t e_ = cudaFuncSetAttribute(dsa::head_rows_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                    (int)sizeof(dsa::HeadRowsBwdSmem));
+        e_ != cudaSuccess)
+      return cuda_fail(e_);
+    attr_done = true;
+  }
+  if (const int st = launch_pdl(false, dsa::head_rows_bwd_kernel, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32),
+                                sizeof(dsa::HeadRowsBwdSmem), stream, p);
       st != DSA_OK || n == 0)
     return st;
   return launch_pdl(true, dsa::head_rows_dg_kernel, dim3((unsigned)(n * q.D / 8)), dim3(256), 0, stream, q);
