@@ -360,7 +360,7 @@ DSA_API int dsa_decode(const void* q_idx, const void* k_idx, const void* w, cons
  * angle is reduced in fp64, so far positions lose nothing), rounded once to bf16.
  *   Q device bf16 [total_q, Hq, d], K device bf16 [total_q, Hk, d] or NULL with Hk = 0;
  *   q_stride, k_stride, ...: elements from one token to the next (>= heads * d, a multiple
- *     of 8), so Q and K may be slices of one fused projection; heads are dense.
+ *     of 8, < 2^31), so Q and K may be slices of one fused projection; heads are dense.
  *   q_weight, k_weight device bf16 [d], each may be NULL;  inv_freq device fp64
  *     [rotary_dim/2], radians per position, or NULL with rotary_dim = 0 (no rotation).
  *   positions device int32 [total_q] or NULL.  NULL: the position of token i of sequence b

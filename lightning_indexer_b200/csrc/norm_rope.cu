@@ -9,10 +9,9 @@
 //   dg = sum over rows of dn * xh,   dx = rstd * (dn * g - xh * mean(dn * g * xh)).
 // Everything is fp32 from the bf16 inputs to the one rounding of each output.
 //
-// The angle in turns, position * inv_freq / (2 pi), is formed in fp64 and reduced there to
-// [-1/2, 1/2] before it becomes fp32: at position 10^6 an fp32 product would be off by 0.06
-// rad, this one by 2e-7 rad.  cos and sin are computed once per token and warp and reused
-// over the token's heads.
+// The angle's fraction of a turn is an integer product (see turn_step): at position 10^6 an
+// fp32 product would be off by 0.06 rad, this one by 1e-7 rad.  cos and sin are computed once
+// per token and warp and reused over the token's heads.
 //
 // Layout: D / 16 lanes hold one row, 16 elements each in two 16-byte pieces chosen so that
 // both members of a rotation pair sit in the same lane, so the only exchange between lanes
@@ -32,7 +31,8 @@ struct HeadSeg {
   const uint16_t* x;    // [T, heads, D], token stride x_stride (elements)
   const uint16_t* dy;   // backward only: gradient at the output, token stride dy_stride
   uint16_t* y;          // output rows (forward), gradient rows (backward)
-  long long x_stride, dy_stride, y_stride;  // y_stride: of a token, or of a page when paged
+  int x_stride, dy_stride;  // elements from token to token
+  long long y_stride;       // the same of the output, or of a page when paged
   const uint16_t* g;    // [D] or null: no norm
   const double* inv_freq;  // [rotary / 2] or null
   int heads, D, rotary;
@@ -40,6 +40,7 @@ struct HeadSeg {
   int block0;           // first block of this tensor's rows
   int groups;           // warp-sized groups of 512 / D rows
   int iters;            // groups of a run (forward: of a warp), at most 32 tokens' worth
+  int warp_iters;       // backward: groups of a warp
   unsigned div_mul;     // row / heads = (row * div_mul) >> div_shift for rows < 2^31
   int div_shift;
   float* dg_part;       // backward with norm: [blocks of this tensor][D]
@@ -64,7 +65,6 @@ constexpr int NR_WARPS = 8;
 struct HeadRowsParams {
   HeadSeg seg[NR_MAX_SEGS];
   int nseg;
-  int warp_iters;  // backward: groups of a warp
   float eps;
   TokenMap tk;
 };
@@ -108,26 +108,79 @@ __device__ __forceinline__ bool place_token(const TokenMap& tk, const HeadSeg& s
   return true;
 }
 
-// cos and sin of pos * inv_freq, the turns reduced in fp64.
-__device__ __forceinline__ void turn(double inv_freq, int pos, float& c, float& s) {
-  double x = (double)pos * (inv_freq * 0.15915494309189533577);
-  x -= rint(x);
-  sincospif(2.f * (float)x, &s, &c);
+// Turns per position as a 64-bit binary fraction: position * step, taken modulo 2^64 by the
+// integer product itself, is the angle's fraction of a turn, exact however far the position.
+__device__ __forceinline__ unsigned long long turn_step(double inv_freq) {
+  double y = inv_freq * 0.15915494309189533577;  // radians to turns
+  y -= floor(y);
+  return __double2ull_rn(y * 18446744073709551616.0);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
+// cos and sin of an angle given in 2^-32 turns: the nearest quarter turn is taken off, the
+// rest, at most pi / 4 either way, goes through the Taylor polynomials of both (remainders
+// z^11 / 11! and z^10 / 10!: below 3e-8).
+__device__ __forceinline__ void turn(uint32_t angle, float& c, float& s) {
+  const uint32_t q = (angle + 0x20000000u) >> 30;
+  const float z = (float)(int)(angle - (q << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z2 = z * z;
+  float ps = fmaf(z2, 2.7557319e-6f, -1.9841270e-4f);
+  ps = fmaf(ps, z2, 8.3333333e-3f);
+  ps = fmaf(ps, z2, -1.6666667e-1f);
+  const float sz = fmaf(ps * z2, z, z);
+  float pc = fmaf(z2, 2.4801587e-5f, -1.3888889e-3f);
+  pc = fmaf(pc, z2, 4.1666667e-2f);
+  pc = fmaf(pc, z2, -0.5f);
+  const float cz = fmaf(pc, z2, 1.f);
+  const bool odd = q & 1u;
+  s = __uint_as_float(__float_as_uint(odd ? cz : sz) ^ ((q & 2u) << 30));
+  c = __uint_as_float(__float_as_uint(odd ? sz : cz) ^ (((q + 1u) & 2u) << 30));
+}
+__device__ __forceinline__ uint32_t angle_at(unsigned long long step, int pos) {
+  return (uint32_t)(((unsigned long long)(long long)pos * step) >> 32);
+}
+
+// Two fp32 values in one 64-bit register pair: one instruction does both products, which
+// counts here because the issue slots, not the memory, are what these kernels run out of.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 sub2(F2 a, F2 b) {
+  F2 r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+// eight bf16 <-> four pairs
+__device__ __forceinline__ void unpack8(const uint4& v, F2* f) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
+__device__ __forceinline__ uint4 pack8(const F2* f) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    const float2 x = f2_get(f[i]);
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
     w[i] = *reinterpret_cast<const uint32_t*>(&p);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -162,32 +215,52 @@ struct LaneCols {
   }
 };
 
-// cos and sin of this lane's eight pairs at its row's position.  Where every row of the warp
-// belongs to one token, each of the warp's row groups computes a share and they exchange.
-template <int D, bool INTER>
-__device__ __forceinline__ void lane_turns(const HeadSeg& s, const LaneCols<D, INTER>& col, bool shared, int rg, int pos,
-                                           float* c, float* sn) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR;
-  constexpr int PER = RPW >= 8 ? 1 : 8 / RPW;  // pairs per row group when shared
-  if (shared) {
-    float mc[PER], ms[PER];
+// The turn steps of the block's segment and, per warp, the (cos, sin) of one token's pairs.
+struct TurnSmem {
+  unsigned long long step[64];
+  __align__(16) float2 cs[NR_WARPS][64];
+};
+__device__ __forceinline__ void load_steps(const HeadSeg& s, TurnSmem& ts) {
+  if (!s.inv_freq) return;  // block-uniform
+  if (threadIdx.x < s.rotary / 2) ts.step[threadIdx.x] = turn_step(s.inv_freq[threadIdx.x]);
+  __syncthreads();
+}
+
+// cos and sin of this lane's eight rotation pairs, two by two.
+struct LaneTurns {
+  F2 c[4], s[4];
+};
+
+// This lane's turns at its row's position.  Where every row of the warp belongs to one token,
+// the lanes compute the token's rotary / 2 pairs side by side and exchange them through
+// shared memory.
+template <bool SHARED, bool FULL, int D, bool INTER>
+__device__ __forceinline__ void lane_turns(const HeadSeg& s, const LaneCols<D, INTER>& col, TurnSmem& ts, int pos,
+                                           LaneTurns& L) {
+  const int lane = threadIdx.x % 32;
+  if (SHARED) {
+    float2* cs = ts.cs[threadIdx.x / 32];
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int p = (rg * PER + j) & 7;
-      mc[j] = 1.f, ms[j] = 0.f;
-      if (col.rotates(p)) turn(s.inv_freq[col.freq(p)], pos, mc[j], ms[j]);
-    }
+    for (int j = 0; j < (D + 63) / 64; ++j)
+      if (32 * j + lane < s.rotary / 2) turn(angle_at(ts.step[32 * j + lane], pos), cs[32 * j + lane].x, cs[32 * j + lane].y);
+    __syncwarp();
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const int src = (p / PER) * LPR + col.sub;
-      c[p] = __shfl_sync(0xffffffffu, mc[p % PER], src);
-      sn[p] = __shfl_sync(0xffffffffu, ms[p % PER], src);
+    for (int p = 0; p < 8; p += 2) {
+      const float4 v = FULL || col.rotates(p) ? *reinterpret_cast<const float4*>(cs + col.freq(p)) : make_float4(1.f, 0.f, 1.f, 0.f);
+      L.c[p / 2] = f2(v.x, v.z);
+      L.s[p / 2] = f2(v.y, v.w);
     }
   } else {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      c[p] = 1.f, sn[p] = 0.f;
-      if (col.rotates(p)) turn(s.inv_freq[col.freq(p)], pos, c[p], sn[p]);
+    for (int p = 0; p < 8; p += 2) {
+      float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
+      if (col.rotates(p)) {
+        turn(angle_at(ts.step[col.freq(p)], pos), c0, s0);
+        turn(angle_at(ts.step[col.freq(p) + 1], pos), c1, s1);
+      }
+      L.c[p / 2] = f2(c0, c1);
+      L.s[p / 2] = f2(s0, s1);
     }
   }
 }
@@ -199,19 +272,25 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// Pair rotation of the lane's 16 values (two pieces) by the angles (c, sgn * sn).
-template <bool INTER>
-__device__ __forceinline__ void rotate16(float* a, float* b, bool rot0, bool rot1, const float* c, const float* sn, float sgn) {
+// Pair rotation of the lane's 16 values (two pieces) by the turns' angles, or back by them.
+template <bool INTER, bool BACK>
+__device__ __forceinline__ void rotate16(F2* a, F2* b, bool rot0, bool rot1, const LaneTurns& L) {
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if (!(half ? rot1 : rot0)) continue;  // dims that pass stay out of every product
 #pragma unroll
-    for (int p = 4 * half; p < 4 * half + 4; ++p) {
-      float& u = INTER ? (p < 4 ? a[2 * (p & 3)] : b[2 * (p & 3)]) : a[p];
-      float& v = INTER ? (p < 4 ? a[2 * (p & 3) + 1] : b[2 * (p & 3) + 1]) : b[p];
-      const float s = sgn * sn[p], u0 = u, v0 = v;
-      u = fmaf(u0, c[p], -(v0 * s));
-      v = fmaf(v0, c[p], u0 * s);
+    for (int i = 2 * half; i < 2 * half + 2; ++i) {
+      if (INTER) {  // pairs 2 i and 2 i + 1: the words 2 (i & 1) and 2 (i & 1) + 1 of this half's piece
+        const float2 c = f2_get(L.c[i]), sn = f2_get(L.s[i]), s = BACK ? make_float2(-sn.x, -sn.y) : sn;
+        F2* x = (half ? b : a) + 2 * (i & 1);
+        const float2 x0 = f2_get(x[0]), x1 = f2_get(x[1]);
+        x[0] = f2(fmaf(x0.x, c.x, -(x0.y * s.x)), fmaf(x0.y, c.x, x0.x * s.x));
+        x[1] = f2(fmaf(x1.x, c.y, -(x1.y * s.y)), fmaf(x1.y, c.y, x1.x * s.y));
+      } else {
+        const F2 u = a[i], v = b[i];
+        a[i] = BACK ? fma2(u, L.c[i], mul2(v, L.s[i])) : sub2(mul2(u, L.c[i]), mul2(v, L.s[i]));
+        b[i] = BACK ? sub2(mul2(v, L.c[i]), mul2(u, L.s[i])) : fma2(v, L.c[i], mul2(u, L.s[i]));
+      }
     }
   }
 }
@@ -237,87 +316,119 @@ struct RunPlaces {
   }
 };
 
-constexpr int NR_FWD_STAGES = 4;  // groups in flight per warp
+// How a tensor's rows are walked.  ROWS_ANY: a group may straddle tokens.  ROWS_TOKEN: the
+// heads fill whole groups, so a group's rows share their token and its turns.  ROWS_FULL: the
+// same, with a norm and every dim rotating (no case left to test in the loop).
+enum RowsMode { ROWS_ANY, ROWS_TOKEN, ROWS_FULL };
+__device__ __forceinline__ int rows_mode(const HeadSeg& s) {
+  return s.heads * s.D % 512 != 0 ? ROWS_ANY : s.g && s.inv_freq && s.rotary == s.D ? ROWS_FULL : ROWS_TOKEN;
+}
+
+constexpr int NR_STAGES = 4;  // groups in flight per warp
 constexpr int NR_GROUP_BYTES = 1024;
 
-template <int D, bool INTER>
+// A lane's row as the warp steps through its groups.  SHARED: the heads fill whole groups, so
+// all rows of a group belong to one token and the token is found by counting.
+template <bool SHARED, int RPW>
+struct RowCursor {
+  unsigned r, h;
+  int t;
+  __device__ __forceinline__ RowCursor(const HeadSeg& s, unsigned row) : r(row) {
+    t = row_token(s, r);
+    h = r - (unsigned)t * (unsigned)s.heads;
+  }
+  __device__ __forceinline__ void step(const HeadSeg& s) {
+    r += RPW;
+    if (SHARED) {
+      h += RPW;
+      if (h >= (unsigned)s.heads) h -= (unsigned)s.heads, ++t;
+    } else {
+      t = row_token(s, r);
+      h = r - (unsigned)t * (unsigned)s.heads;
+    }
+  }
+};
+
+template <int D, bool INTER, int MODE>
 __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane,
-                                              uint8_t* ring) {
+                                              uint8_t* ring, TurnSmem& ts) {
   using L = LaneCols<D, INTER>;
-  constexpr int S = NR_FWD_STAGES;
+  constexpr bool SHARED = MODE != ROWS_ANY, FULL = MODE == ROWS_FULL;
+  constexpr int S = NR_STAGES;
   const int sub = lane % L::LPR, rg = lane / L::LPR;
   const L col(s, sub);
-  const unsigned H = s.heads;
-  const bool shared = H % L::RPW == 0;
-  const unsigned rows = (unsigned)p.tk.T * H;
+  const bool norm = FULL || s.g != nullptr, turned = FULL || s.inv_freq != nullptr;
+  const unsigned rows = (unsigned)p.tk.T * (unsigned)s.heads;
   const int grp0 = warp_in_seg * s.iters, n = min(s.iters, s.groups - grp0);
-  if (n <= 0) return;
-  const unsigned row0 = (unsigned)grp0 * L::RPW;
-  uint8_t* mine = ring + lane * 16;
-  auto issue = [&](int it) {
-    const unsigned r = row0 + it * L::RPW + rg;
-    if (it < n && r < rows) {
-      const int t = row_token(s, r);
-      const uint16_t* src = s.x + (long long)t * s.x_stride + (r - (unsigned)t * H) * D;
-      const uint32_t dst = smem_u32(mine + (it % S) * NR_GROUP_BYTES);
-      cp_async_16(dst, src + col.e0, true);
-      cp_async_16(dst + 512, src + col.e1, true);
+  const unsigned row0 = (unsigned)grp0 * L::RPW, row_end = n > 0 ? min(row0 + n * L::RPW, rows) : row0;
+  const uint32_t mine = smem_u32(ring) + lane * 16;
+  const int de = col.e1 - col.e0;
+  RowCursor<SHARED, L::RPW> ahead(s, row0 + rg), at = ahead;
+  uint32_t fill = 0, use = 0;
+  auto issue = [&] {
+    if (ahead.r < row_end) {
+      const uint16_t* src = s.x + (long long)ahead.t * s.x_stride + (int)(ahead.h * D + col.e0);
+      cp_async_16(mine + fill, src, true);
+      cp_async_16(mine + fill + 512, src + de, true);
     }
     cp_async_commit();
+    ahead.step(s);
+    fill = (fill + NR_GROUP_BYTES) & (S * NR_GROUP_BYTES - 1);
   };
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
-  const int t_first = row_token(s, row0), t_last = row_token(s, min(row0 + n * L::RPW, rows) - 1);
+  for (int i = 0; i < S - 1; ++i) issue();
+  const int t_first = row_token(s, row0), t_last = n > 0 ? row_token(s, row_end - 1) : t_first - 1;
   RunPlaces all, cur;
   all.look_up(p.tk, s, t_first, t_last, lane);
   uint4 ga = {}, gb = {};
-  if (s.g) {
+  if (norm) {
     ga = *reinterpret_cast<const uint4*>(s.g + col.e0);
     gb = *reinterpret_cast<const uint4*>(s.g + col.e1);
   }
-  float g0[8], g1[8];
+  F2 g0[4], g1[4];
   unpack8(ga, g0);
   unpack8(gb, g1);
-  float c[8], sn[8];
+  load_steps(s, ts);
+  LaneTurns turns;
   int cur_t = -1;
 #pragma unroll 1
   for (int it = 0; it < n; ++it) {
-    issue(it + S - 1);
-    const unsigned r = row0 + it * L::RPW + rg;
-    const int t = r < rows ? row_token(s, r) : t_last;
-    const unsigned h = r - (unsigned)t * H;
-    if (__any_sync(0xffffffffu, t != cur_t)) {
+    issue();
+    const bool in = SHARED || at.r < row_end;
+    const int t = in ? at.t : t_last;
+    if (SHARED ? t != cur_t : __any_sync(0xffffffffu, t != cur_t)) {
       cur_t = t;
       cur.take(all, t - t_first);
-      if (s.inv_freq) lane_turns(s, col, shared, rg, cur.pos, c, sn);
+      if (turned) lane_turns<SHARED, FULL>(s, col, ts, cur.pos, turns);
     }
     cp_async_wait<S - 1>();
-    uint4 xa = *reinterpret_cast<const uint4*>(mine + (it % S) * NR_GROUP_BYTES);
-    uint4 xb = *reinterpret_cast<const uint4*>(mine + (it % S) * NR_GROUP_BYTES + 512);
-    if (s.g || s.inv_freq) {  // else the rows pass as they are
-      float a[8], b[8];
+    const uint8_t* st = ring + lane * 16 + use;
+    uint4 xa = *reinterpret_cast<const uint4*>(st), xb = *reinterpret_cast<const uint4*>(st + 512);
+    if (norm || turned) {  // else the rows pass as they are
+      F2 a[4], b[4];
       unpack8(xa, a);
       unpack8(xb, b);
-      if (s.g) {
-        float ss = 0.f, st = 0.f;
+      if (norm) {
+        F2 ss = f2(0.f, 0.f), st2 = ss;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss), st = fmaf(b[i], b[i], st);
-        const float rstd = rsqrtf(row_sum<L::LPR>(ss + st) * (1.f / D) + p.eps);
+        for (int i = 0; i < 4; ++i) ss = fma2(a[i], a[i], ss), st2 = fma2(b[i], b[i], st2);
+        const float2 x = f2_get(ss), y = f2_get(st2);
+        const float rstd = rsqrtf(row_sum<L::LPR>((x.x + x.y) + (y.x + y.y)) * (1.f / D) + p.eps);
+        const F2 rr = f2(rstd, rstd);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a[i] *= rstd * g0[i];
-          b[i] *= rstd * g1[i];
-        }
+        for (int i = 0; i < 4; ++i) a[i] = mul2(mul2(a[i], rr), g0[i]), b[i] = mul2(mul2(b[i], rr), g1[i]);
       }
-      rotate16<INTER>(a, b, col.rot0, col.rot1, c, sn, 1.f);
+      rotate16<INTER, false>(a, b, FULL || col.rot0, FULL || col.rot1, turns);
       xa = pack8(a);
       xb = pack8(b);
     }
-    if (cur.ok && r < rows) {
-      uint16_t* dst = s.y + cur.yoff + h * D;
-      *reinterpret_cast<uint4*>(dst + col.e0) = xa;
-      *reinterpret_cast<uint4*>(dst + col.e1) = xb;
+    if (cur.ok && in) {
+      uint16_t* dst = s.y + cur.yoff + (int)(at.h * D + col.e0);
+      *reinterpret_cast<uint4*>(dst) = xa;
+      *reinterpret_cast<uint4*>(dst + de) = xb;
     }
+    at.step(s);
+    use = (use + NR_GROUP_BYTES) & (S * NR_GROUP_BYTES - 1);
   }
   cp_async_wait<0>();
 }
@@ -330,65 +441,73 @@ __device__ __forceinline__ int block_seg(const HeadRowsParams& p) {
   return i;
 }
 
+// D and INTER (0 or 1) of every segment where they agree, else 0 and -1: the call is then
+// dispatched per segment, at the registers of the largest form.
+template <int D, int INTER>
 __global__ void __launch_bounds__(NR_WARPS * 32, 3) head_rows_fwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ __align__(16) uint8_t rings[NR_WARPS][NR_FWD_STAGES * NR_GROUP_BYTES];
+  __shared__ __align__(16) uint8_t rings[NR_WARPS][NR_STAGES * NR_GROUP_BYTES];
+  __shared__ TurnSmem ts;
   const HeadSeg& s = p.seg[block_seg(p)];
   const int w = ((int)blockIdx.x - s.block0) * NR_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
   uint8_t* ring = rings[threadIdx.x / 32];
-  if (s.interleaved) {
-    if (s.D == 128) head_rows_fwd<128, true>(p, s, w, lane, ring);
-    else if (s.D == 64) head_rows_fwd<64, true>(p, s, w, lane, ring);
-    else head_rows_fwd<32, true>(p, s, w, lane, ring);
-  } else {
-    if (s.D == 128) head_rows_fwd<128, false>(p, s, w, lane, ring);
-    else if (s.D == 64) head_rows_fwd<64, false>(p, s, w, lane, ring);
-    else head_rows_fwd<32, false>(p, s, w, lane, ring);
+  const int mode = rows_mode(s);
+#define DSA_HEAD_ROWS(DD, II)                                                            \
+  if ((D == 0 || D == DD) && (INTER < 0 || INTER == II) && s.D == DD && s.interleaved == II) { \
+    if (mode == ROWS_FULL) head_rows_fwd<DD, II, ROWS_FULL>(p, s, w, lane, ring, ts);    \
+    else if (mode == ROWS_TOKEN) head_rows_fwd<DD, II, ROWS_TOKEN>(p, s, w, lane, ring, ts); \
+    else head_rows_fwd<DD, II, ROWS_ANY>(p, s, w, lane, ring, ts);                       \
   }
+  DSA_HEAD_ROWS(128, 0) DSA_HEAD_ROWS(128, 1) DSA_HEAD_ROWS(64, 0) DSA_HEAD_ROWS(64, 1) DSA_HEAD_ROWS(32, 0) DSA_HEAD_ROWS(32, 1)
+#undef DSA_HEAD_ROWS
 }
 
-constexpr int NR_BWD_STAGES = 3;  // groups in flight per warp, of x and of dy
-
-template <int D, bool INTER>
+template <int D, bool INTER, int MODE>
 __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane,
-                                              uint8_t* ring, float* acc_smem) {
+                                              uint8_t* ring, TurnSmem& ts, float* acc_smem) {
   using L = LaneCols<D, INTER>;
-  constexpr int S = NR_BWD_STAGES;
+  constexpr bool SHARED = MODE != ROWS_ANY, FULL = MODE == ROWS_FULL;
+  constexpr int S = NR_STAGES;
   const int sub = lane % L::LPR, rg = lane / L::LPR;
   const L col(s, sub);
-  const unsigned H = s.heads;
-  const bool shared = H % L::RPW == 0;
-  const unsigned rows = (unsigned)p.tk.T * H;
-  const int grp0 = (int)min((long long)warp_in_seg * p.warp_iters, (long long)s.groups);
-  const int n = min(p.warp_iters, s.groups - grp0);
-  const unsigned row0 = (unsigned)grp0 * L::RPW;
-  uint8_t* mine = ring + lane * 16;
-  auto issue = [&](int it) {
-    const unsigned r = row0 + it * L::RPW + rg;
-    if (it < n && r < rows) {
-      const int t = row_token(s, r);
-      const unsigned h = r - (unsigned)t * H;
-      const uint32_t dst = smem_u32(mine + (it % S) * 2 * NR_GROUP_BYTES);
-      const uint16_t* src = s.dy + (long long)t * s.dy_stride + h * D;
-      cp_async_16(dst, src + col.e0, true);
-      cp_async_16(dst + 512, src + col.e1, true);
-      if (s.g) {
-        src = s.x + (long long)t * s.x_stride + h * D;
-        cp_async_16(dst + 1024, src + col.e0, true);
-        cp_async_16(dst + 1536, src + col.e1, true);
+  const bool norm = FULL || s.g != nullptr, turned = FULL || s.inv_freq != nullptr;
+  const unsigned rows = (unsigned)p.tk.T * (unsigned)s.heads;
+  const int grp0 = (int)min((long long)warp_in_seg * s.warp_iters, (long long)s.groups);
+  const int n = min(s.warp_iters, s.groups - grp0);
+  const unsigned row0 = (unsigned)grp0 * L::RPW, row_end = min(row0 + n * L::RPW, rows);
+  const uint32_t mine = smem_u32(ring) + lane * 16;
+  const int de = col.e1 - col.e0;
+  RowCursor<SHARED, L::RPW> ahead(s, row0 + rg), at = ahead;
+  uint32_t fill = 0, use = 0;
+  auto issue = [&] {
+    if (ahead.r < row_end) {
+      const int in_token = (int)(ahead.h * D + col.e0);
+      const uint16_t* src = s.dy + (long long)ahead.t * s.dy_stride + in_token;
+      cp_async_16(mine + fill, src, true);
+      cp_async_16(mine + fill + 512, src + de, true);
+      if (norm) {
+        src = s.x + (long long)ahead.t * s.x_stride + in_token;
+        cp_async_16(mine + fill + 1024, src, true);
+        cp_async_16(mine + fill + 1536, src + de, true);
       }
     }
     cp_async_commit();
+    ahead.step(s);
+    fill = (fill + 2 * NR_GROUP_BYTES) & (2 * S * NR_GROUP_BYTES - 1);
   };
 #pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue(i);
+  for (int i = 0; i < S - 1; ++i) issue();
   uint4 ga = {}, gb = {};
-  if (s.g) {
+  if (norm) {
     ga = *reinterpret_cast<const uint4*>(s.g + col.e0);
     gb = *reinterpret_cast<const uint4*>(s.g + col.e1);
   }
-  float dg0[8] = {}, dg1[8] = {}, c[8], sn[8];
+  load_steps(s, ts);
+  F2 dg0[4], dg1[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dg0[i] = dg1[i] = f2(0.f, 0.f);
+  LaneTurns turns;
   RunPlaces all, cur;
   int cur_t = -1, t_first = 0, run_end = 0;
 #pragma unroll 1
@@ -398,72 +517,81 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
       t_first = row_token(s, row0 + it * L::RPW);
       all.look_up(p.tk, s, t_first, row_token(s, min(row0 + run_end * L::RPW, rows) - 1), lane);
     }
-    issue(it + S - 1);
-    const unsigned r = row0 + it * L::RPW + rg;
-    const bool in = r < rows;
-    const int t = in ? row_token(s, r) : t_first;
-    const unsigned h = r - (unsigned)t * H;
-    if (__any_sync(0xffffffffu, t != cur_t)) {
+    issue();
+    const bool in = SHARED || at.r < row_end;
+    const int t = in ? at.t : t_first;
+    if (SHARED ? t != cur_t : __any_sync(0xffffffffu, t != cur_t)) {
       cur_t = t;
       cur.take(all, t - t_first);
-      if (s.inv_freq) lane_turns(s, col, shared, rg, cur.pos, c, sn);
+      if (turned) lane_turns<SHARED, FULL>(s, col, ts, cur.pos, turns);
     }
     const bool ok = cur.ok && in;
     cp_async_wait<S - 1>();
-    const uint4* st = reinterpret_cast<const uint4*>(mine + (it % S) * 2 * NR_GROUP_BYTES);
-    float a[8], b[8];
+    if (FULL && !ok) {  // the whole group's token
+      at.step(s);
+      use = (use + 2 * NR_GROUP_BYTES) & (2 * S * NR_GROUP_BYTES - 1);
+      continue;
+    }
+    const uint4* st = reinterpret_cast<const uint4*>(ring + lane * 16 + use);
+    F2 a[4], b[4];
     unpack8(st[0], a);
     unpack8(st[32], b);
-    rotate16<INTER>(a, b, col.rot0, col.rot1, c, sn, -1.f);
-    if (s.g) {
-      float xf[8], xg[8], g[8];
-      unpack8(st[64], xf);
-      unpack8(st[96], xg);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(xf[i], xf[i], fmaf(xg[i], xg[i], ss));
-      const float rstd = rsqrtf(row_sum<L::LPR>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) xf[i] *= rstd, xg[i] *= rstd;  // xh
-      if (ok) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dg0[i] = fmaf(a[i], xf[i], dg0[i]), dg1[i] = fmaf(b[i], xg[i], dg1[i]);
-      }
+    rotate16<INTER, true>(a, b, FULL || col.rot0, FULL || col.rot1, turns);  // dn
+    if (norm) {
+      F2 x0[4], x1[4], g[4], ss = f2(0.f, 0.f), st2 = ss, dot = ss, dot2 = ss, m0[4], m1[4];
+      unpack8(st[64], x0);
+      unpack8(st[96], x1);
       unpack8(ga, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] *= g[i], dot = fmaf(a[i], xf[i], dot);
+      for (int i = 0; i < 4; ++i) m0[i] = mul2(a[i], g[i]), ss = fma2(x0[i], x0[i], ss), dot = fma2(m0[i], x0[i], dot);
       unpack8(gb, g);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] *= g[i], dot = fmaf(b[i], xg[i], dot);
-      const float mean = row_sum<L::LPR>(dot) * (1.f / D);
+      for (int i = 0; i < 4; ++i) m1[i] = mul2(b[i], g[i]), st2 = fma2(x1[i], x1[i], st2), dot2 = fma2(m1[i], x1[i], dot2);
+      const float2 sa = f2_get(ss), sb = f2_get(st2), da = f2_get(dot), db = f2_get(dot2);
+      float sum = (sa.x + sa.y) + (sb.x + sb.y), prod = (da.x + da.y) + (db.x + db.y);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        a[i] = rstd * fmaf(-xf[i], mean, a[i]);
-        b[i] = rstd * fmaf(-xg[i], mean, b[i]);
+      for (int o = 1; o < L::LPR; o <<= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        prod += __shfl_xor_sync(0xffffffffu, prod, o);
+      }
+      // dg += dn x rstd;  dx = rstd (dn g - x rstd^2 mean(dn g x))
+      const float rstd = rsqrtf(sum * (1.f / D) + p.eps);
+      const float back = -(prod * (1.f / D)) * rstd * rstd;
+      const F2 rr = f2(rstd, rstd), bb = f2(back, back);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (FULL || ok) {
+          dg0[i] = fma2(mul2(a[i], rr), x0[i], dg0[i]);
+          dg1[i] = fma2(mul2(b[i], rr), x1[i], dg1[i]);
+        }
+        a[i] = mul2(rr, fma2(x0[i], bb, m0[i]));
+        b[i] = mul2(rr, fma2(x1[i], bb, m1[i]));
       }
     }
     if (ok) {
-      uint16_t* dst = s.y + cur.yoff + h * D;
-      *reinterpret_cast<uint4*>(dst + col.e0) = pack8(a);
-      *reinterpret_cast<uint4*>(dst + col.e1) = pack8(b);
+      uint16_t* dst = s.y + cur.yoff + (int)(at.h * D + col.e0);
+      *reinterpret_cast<uint4*>(dst) = pack8(a);
+      *reinterpret_cast<uint4*>(dst + de) = pack8(b);
     }
+    at.step(s);
+    use = (use + 2 * NR_GROUP_BYTES) & (2 * S * NR_GROUP_BYTES - 1);
   }
   cp_async_wait<0>();
   if (!s.g) return;  // block-uniform
   // the block's share of dg: rows of the warp, then the warps in order
-#pragma unroll
-  for (int o = L::LPR; o < 32; o <<= 1)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dg0[i] += __shfl_xor_sync(0xffffffffu, dg0[i], o);
-      dg1[i] += __shfl_xor_sync(0xffffffffu, dg1[i], o);
-    }
   const int warp = threadIdx.x / 32;
-  if (rg == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      acc_smem[warp * D + col.e0 + i] = dg0[i];
-      acc_smem[warp * D + col.e1 + i] = dg1[i];
+  for (int i = 0; i < 8; ++i) {
+    const float2 u = f2_get(dg0[i / 2]), v = f2_get(dg1[i / 2]);
+    float x = i & 1 ? u.y : u.x, y = i & 1 ? v.y : v.x;
+#pragma unroll
+    for (int o = L::LPR; o < 32; o <<= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if (rg == 0) {
+      acc_smem[warp * D + col.e0 + i] = x;
+      acc_smem[warp * D + col.e1 + i] = y;
     }
   }
   __syncthreads();
@@ -476,10 +604,12 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
 }
 
 struct HeadRowsBwdSmem {
-  __align__(16) uint8_t rings[NR_WARPS][NR_BWD_STAGES * 2 * NR_GROUP_BYTES];
+  __align__(16) uint8_t rings[NR_WARPS][NR_STAGES * 2 * NR_GROUP_BYTES];
+  TurnSmem ts;
   float acc[NR_WARPS * 128];
 };
 
+template <int D, int INTER>
 __global__ void __launch_bounds__(NR_WARPS * 32, 2) head_rows_bwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
@@ -488,15 +618,10 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 2) head_rows_bwd_kernel(const _
   const HeadSeg& s = p.seg[block_seg(p)];
   const int w = ((int)blockIdx.x - s.block0) * NR_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
   uint8_t* ring = sm.rings[threadIdx.x / 32];
-  if (s.interleaved) {
-    if (s.D == 128) head_rows_bwd<128, true>(p, s, w, lane, ring, sm.acc);
-    else if (s.D == 64) head_rows_bwd<64, true>(p, s, w, lane, ring, sm.acc);
-    else head_rows_bwd<32, true>(p, s, w, lane, ring, sm.acc);
-  } else {
-    if (s.D == 128) head_rows_bwd<128, false>(p, s, w, lane, ring, sm.acc);
-    else if (s.D == 64) head_rows_bwd<64, false>(p, s, w, lane, ring, sm.acc);
-    else head_rows_bwd<32, false>(p, s, w, lane, ring, sm.acc);
-  }
+  const int mode = rows_mode(s);
+  if (mode == ROWS_FULL) head_rows_bwd<D, INTER, ROWS_FULL>(p, s, w, lane, ring, sm.ts, sm.acc);
+  else if (mode == ROWS_TOKEN) head_rows_bwd<D, INTER, ROWS_TOKEN>(p, s, w, lane, ring, sm.ts, sm.acc);
+  else head_rows_bwd<D, INTER, ROWS_ANY>(p, s, w, lane, ring, sm.ts, sm.acc);
 }
 
 // dg of up to two tensors from their blocks' shares, always in the same order: one block per
@@ -533,9 +658,9 @@ static long long seg_groups(const dsa::HeadRowsParams& p, const dsa::HeadSeg& s)
   const long long rpw = 512 / s.D;
   return ((long long)p.tk.T * s.heads + rpw - 1) / rpw;
 }
-// Fills in what the kernels read of each segment; a warp takes warp_iters groups, or where
-// that is 0 as many as make a run.  Returns the number of blocks.
-static int plan_segs(dsa::HeadRowsParams& p, int run, int warp_iters) {
+// Fills in what the kernels read of each segment; a warp takes s.warp_iters groups where that
+// is set, else one run.  Returns the number of blocks.
+static int plan_segs(dsa::HeadRowsParams& p, int run) {
   long long block = 0;
   for (int i = 0; i < p.nseg; ++i) {
     dsa::HeadSeg& s = p.seg[i];
@@ -548,7 +673,7 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, int warp_iters) {
     s.div_shift = 31 + lg;
     s.div_mul = (unsigned)(((1ULL << (31 + lg)) + s.heads - 1) / s.heads);
     s.block0 = (int)block;
-    const long long per_block = (long long)(warp_iters ? warp_iters : s.iters) * dsa::NR_WARPS;
+    const long long per_block = (long long)(s.warp_iters ? s.warp_iters : s.iters) * dsa::NR_WARPS;
     block += (s.groups + per_block - 1) / per_block;
   }
   return (int)block;
@@ -557,25 +682,58 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, int warp_iters) {
 int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) {
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
-  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1, 0);
-  return launch_pdl(pdl, dsa::head_rows_fwd_kernel, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), 0, stream, p);
+  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1);
+  int d = p.seg[0].D, inter = p.seg[0].interleaved;
+  for (int i = 1; i < p.nseg; ++i) {
+    if (p.seg[i].D != d || p.seg[i].interleaved != inter) d = 0;
+  }
+  auto kern = d == 128 && inter ? dsa::head_rows_fwd_kernel<128, 1>
+              : d == 128        ? dsa::head_rows_fwd_kernel<128, 0>
+              : d == 64 && inter ? dsa::head_rows_fwd_kernel<64, 1>
+              : d == 64          ? dsa::head_rows_fwd_kernel<64, 0>
+              : d == 32 && inter ? dsa::head_rows_fwd_kernel<32, 1>
+              : d == 32          ? dsa::head_rows_fwd_kernel<32, 0>
+                                 : dsa::head_rows_fwd_kernel<0, -1>;
+  return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), 0, stream, p);
 }
 
-// Groups per warp of the backward: the whole call in at most 16 warps' worth per SM.
-static int bwd_iters(long long groups) {
-  const long long warps = 16LL * sm_count();
-  return (int)std::max<long long>(1, (groups + warps - 1) / warps);
+// Groups per warp of the backward, so that the whole call is at most 16 warps' worth per SM.
+// A token's turns cost about 0.4 of a group and are paid once per token and warp: tensors with
+// few heads get fewer groups per warp.
+static int bwd_weight(int heads, int d) { return 10 + 4 * (512 / d) / std::max(heads, 512 / d); }
+static int bwd_iters(long long T, int Hq, int Hk, int d, int heads) {
+  const long long rpw = 512 / d, nq = (T * Hq + rpw - 1) / rpw, nk = (T * Hk + rpw - 1) / rpw;
+  const long long warps = 15LL * sm_count();  // the last block of each tensor may be part empty
+  const long long budget = (nq * bwd_weight(Hq, d) + (Hk ? nk * bwd_weight(Hk, d) : 0) + warps - 1) / warps;
+  return (int)std::max<long long>(1, (budget + bwd_weight(heads, d) - 1) / bwd_weight(heads, d));
 }
 size_t norm_rope_bwd_ws_bytes(long long T, int Hq, int Hk, int d) {
-  const long long rpw = 512 / d, nq = (T * Hq + rpw - 1) / rpw, nk = (T * Hk + rpw - 1) / rpw;
-  const long long per_block = (long long)bwd_iters(nq + nk) * dsa::NR_WARPS;
-  return (size_t)((nq + per_block - 1) / per_block + (nk + per_block - 1) / per_block) * d * sizeof(float);
+  const long long rpw = 512 / d;
+  long long blocks = 0;
+  for (int H : {Hq, Hk}) {
+    if (H == 0) continue;
+    const long long per_block = (long long)bwd_iters(T, Hq, Hk, d, H) * dsa::NR_WARPS;
+    blocks += ((T * H + rpw - 1) / rpw + per_block - 1) / per_block;
+  }
+  return (size_t)blocks * d * sizeof(float);
 }
+template <int D, int INTER>
+static int head_rows_bwd_kernel_launch(const dsa::HeadRowsParams& p, int blocks, cudaStream_t stream) {
+  auto kern = dsa::head_rows_bwd_kernel<D, INTER>;
+  constexpr int smem = (int)sizeof(dsa::HeadRowsBwdSmem);
+  static DeviceFlag attr_done;
+  if (!attr_done) {
+    if (const cudaError_t e_ = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e_ != cudaSuccess) return cuda_fail(e_);
+    attr_done = true;
+  }
+  return launch_pdl(false, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), smem, stream, p);
+}
+
 int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], cudaStream_t stream) {
-  long long groups = 0;
-  for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
-  p.warp_iters = bwd_iters(groups);
-  const int blocks = plan_segs(p, 8, p.warp_iters);
+  const int Hk = p.nseg > 1 ? p.seg[1].heads : 0;
+  for (int i = 0; i < p.nseg; ++i)
+    p.seg[i].warp_iters = bwd_iters(p.tk.T, p.seg[0].heads, Hk, p.seg[i].D, p.seg[i].heads);
+  const int blocks = plan_segs(p, 8);
   dsa::DgParams q{};
   int n = 0;
   for (int i = 0; i < p.nseg; ++i) {
@@ -587,18 +745,11 @@ int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], 
     q.blocks[n++] = (i + 1 < p.nseg ? p.seg[i + 1].block0 : blocks) - s.block0;
     q.D = s.D;
   }
-  static DeviceFlag attr_done;
-  if (!attr_done) {
-    if (const cudaError_t e_ = cudaFuncSetAttribute(dsa::head_rows_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                    (int)sizeof(dsa::HeadRowsBwdSmem));
-        e_ != cudaSuccess)
-      return cuda_fail(e_);
-    attr_done = true;
-  }
-  if (const int st = launch_pdl(false, dsa::head_rows_bwd_kernel, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32),
-                                sizeof(dsa::HeadRowsBwdSmem), stream, p);
-      st != DSA_OK || n == 0)
-    return st;
+  const int d = p.seg[0].D, inter = p.seg[0].interleaved;
+  const int st = d == 128 ? (inter ? head_rows_bwd_kernel_launch<128, 1>(p, blocks, stream) : head_rows_bwd_kernel_launch<128, 0>(p, blocks, stream))
+                 : d == 64 ? (inter ? head_rows_bwd_kernel_launch<64, 1>(p, blocks, stream) : head_rows_bwd_kernel_launch<64, 0>(p, blocks, stream))
+                           : (inter ? head_rows_bwd_kernel_launch<32, 1>(p, blocks, stream) : head_rows_bwd_kernel_launch<32, 0>(p, blocks, stream));
+  if (st != DSA_OK || n == 0) return st;
   return launch_pdl(true, dsa::head_rows_dg_kernel, dim3((unsigned)(n * q.D / 8)), dim3(256), 0, stream, q);
 }
 

@@ -12,7 +12,7 @@ static bool rope_args_ok(const double* inv_freq, int rotary_dim, int d) {
   return rotary_dim > 0 && rotary_dim <= d;
 }
 static bool rows_ok(const void* x, int64_t stride, int64_t heads, int d) {
-  return x && aligned16(x) && stride >= heads * d && stride % 8 == 0;
+  return x && aligned16(x) && stride >= heads * d && stride % 8 == 0 && stride <= 0x7FFFFFFFLL;
 }
 static bool head_dim_supported(int d) { return d == 32 || d == 64 || d == 128; }
 static bool page_size_supported(int page_size) {
@@ -28,7 +28,7 @@ static dsa::HeadSeg head_seg(const void* x, int64_t x_stride, const void* weight
                              int interleaved, int heads, int d, void* y, int64_t y_stride) {
   dsa::HeadSeg s{};
   s.x = static_cast<const uint16_t*>(x);
-  s.x_stride = x_stride;
+  s.x_stride = (int)x_stride;
   s.y = static_cast<uint16_t*>(y);
   s.y_stride = y_stride;
   s.g = static_cast<const uint16_t*>(weight);
@@ -111,11 +111,12 @@ static void paged_segs(dsa::HeadRowsParams& p, const void* K, int64_t k_stride, 
                        void* v_cache, int64_t v_page_stride, void* ki_cache, int64_t ki_page_stride,
                        const int32_t* table, int max_pages, int num_pages, int page_size) {
   const int first = p.nseg;
-  p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary, interleaved, Hkv, d, k_cache, k_page_stride);
-  p.seg[p.nseg++] = head_seg(V, v_stride, nullptr, nullptr, 0, 0, Hkv, d, v_cache, v_page_stride);
+  // the rows that cost most go first, the plain copies fill up behind them
   if (k_idx)
     p.seg[p.nseg++] = head_seg(k_idx, ki_stride, k_idx_weight, idx_inv_freq, idx_rotary, idx_interleaved, 1, d_I,
                                ki_cache, ki_page_stride);
+  p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary, interleaved, Hkv, d, k_cache, k_page_stride);
+  p.seg[p.nseg++] = head_seg(V, v_stride, nullptr, nullptr, 0, 0, Hkv, d, v_cache, v_page_stride);
   for (int i = first; i < p.nseg; ++i) p.seg[i].paged = 1;
   p.tk.table = table;
   p.tk.table_width = max_pages;
@@ -326,12 +327,12 @@ DSA_API int dsa_norm_rope_bwd(const void* Q, int64_t q_stride, const void* K, in
   float* dg[2] = {dq_weight, dk_weight};
   p.seg[0] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, dQ, dq_stride);
   p.seg[0].dy = static_cast<const uint16_t*>(dQ_out);
-  p.seg[0].dy_stride = dq_out_stride;
+  p.seg[0].dy_stride = (int)dq_out_stride;
   p.nseg = 1;
   if (K) {
     p.seg[1] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, dK, dk_stride);
     p.seg[1].dy = static_cast<const uint16_t*>(dK_out);
-    p.seg[1].dy_stride = dk_out_stride;
+    p.seg[1].dy_stride = (int)dk_out_stride;
     p.nseg = 2;
   }
   return head_rows_bwd_launch(p, static_cast<float*>(workspace), dg, s);

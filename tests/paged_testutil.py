@@ -34,9 +34,9 @@ def norm_rope_tolerance(x, g, eps, y):
     The output's rounding is at most 2^-8 |y| (half a bf16 step).  Before it, in fp32: the sum of
     128 squares, in chains of 16 joined by 3, is off by (16 + 3) 2^-24 relative, half of which
     enters the root; rsqrtf by 2^-22; two products and the pair's two by 2^-24 each: below 1.1e-6 of
-    |n|.  cos and sin: the angle in turns is rounded to fp32 below 1/2, 2^-26 turns = 9.4e-8 rad, and
-    sincospif is off by 2 steps, 1.2e-7.  Over both members of a pair that is 1.4e-6 (|u| + |v|),
-    at most 3e-6 times the row's largest |n|."""
+    |n|.  cos and sin: the angle, at most pi / 4 after its quarter turns, is off by 2^-23 of itself,
+    9.4e-8 rad; the polynomials' remainders are below 3e-8 and their last roundings 2^-23.  Over
+    both members of a pair that is 1.4e-6 (|u| + |v|), at most 3e-6 times the row's largest |n|."""
     return 2.0 ** -8 * y.abs() + 3e-6 * norm(x, g, eps).abs().amax(-1, keepdim=True)
 
 
