@@ -376,74 +376,87 @@ def indexer_kl_loss_sparse(Q, K, q_idx, k_idx, w, indices, cu_seqlens_q, cu_seql
 # pointer (rows, tables, pages) are checked here against one another; the work is enqueued on
 # the tensors' own device, on its current stream.
 
-def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int):
-    """Checks a contiguous tensor's type, device and shape (None: any size)."""
-    if t.dtype != dtype:
+_BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: current_stream() costs 3 us of a decode step's call
+
+
+def _refuse(t: torch.Tensor, name: str, dtype, shape, dev: int, what: str):
+    """Says why a tensor is refused: the checks themselves are one expression each, for speed."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have {what}")
 
 
-def _rows(t: torch.Tensor, name: str, shape, dev: int):
-    """(pointer, token stride) of bf16 rows [T, heads, d] or [T, d] whose heads are dense."""
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 or (len(shape) == 3 and shape[1] > 1 and st[1] != shape[2]):
-        raise ValueError(f"{name} must have dense heads (only the token stride may be larger)")
-    dense = shape[-1] * (shape[1] if len(shape) == 3 else 1)
-    return t.data_ptr(), (st[0] if shape[0] > 1 else dense)
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """Pointer of a contiguous tensor of this type, shape and device."""
+    if t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, dev, "contiguous elements")
+
+
+def _rows(t: torch.Tensor, name: str, T: int, heads: int, d: int, dev: int):
+    """(pointer, token stride) of bf16 rows [T, heads, d] whose heads are dense."""
+    if t.dtype is _BF16 and t.get_device() == dev >= 0 and t.shape == (T, heads, d):
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == d or heads == 1):
+            return t.data_ptr(), (s0 if T > 1 else heads * d)
+    _refuse(t, name, _BF16, (T, heads, d), dev, "dense heads (only the token stride may be larger)")
+
+
+def _flat_rows(t: torch.Tensor, name: str, T: int, d: int, dev: int):
+    """(pointer, token stride) of bf16 rows [T, d]."""
+    if t.dtype is _BF16 and t.get_device() == dev >= 0 and t.shape == (T, d):
+        s0, s1 = t.stride()
+        if s1 == 1:
+            return t.data_ptr(), (s0 if T > 1 else d)
+    _refuse(t, name, _BF16, (T, d), dev, "dense rows (only the token stride may be larger)")
 
 
 def _pool(t: torch.Tensor, name: str, shape, dev: int):
-    """(pointer, page stride) of a cache [pages, page_size, ...] whose pages are dense."""
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    st, dense = t.stride(), 1
-    for n, m in zip(reversed(shape[1:]), reversed(st[1:])):
-        if n > 1 and m != dense:
-            raise ValueError(f"{name} must have dense pages (only the page stride may be larger)")
-        dense *= n
-    return t.data_ptr(), (st[0] if shape[0] > 1 else dense)
+    """(pointer, page stride) of a bf16 cache [pages, page_size, ...] whose pages are dense."""
+    if t.dtype is _BF16 and t.get_device() == dev >= 0 and t.shape == shape:
+        st, dense, ok = t.stride(), 1, True
+        for i in range(len(shape) - 1, 0, -1):
+            ok = ok and (st[i] == dense or shape[i] == 1)
+            dense *= shape[i]
+        if ok:
+            return t.data_ptr(), (st[0] if shape[0] > 1 else dense)
+    _refuse(t, name, _BF16, shape, dev, "dense pages (only the page stride may be larger)")
 
 
 def _launch(dev: int, name: str, *args):
     """Calls an entry point with the current stream of device `dev` as its last argument."""
     if dev == torch.cuda.current_device():
-        call(name, *args, torch.cuda.current_stream().cuda_stream)
+        st = getattr(_lib.load(), name)(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            call(name, *args, torch.cuda.current_stream().cuda_stream)
+            st = getattr(_lib.load(), name)(*args, _raw_stream(dev))
+    if st != 0:
+        raise DSAError(name, st)
 
 
 def _rope(inv_freq, name: str, dev: int):
     """(pointer, rotary_dim) of the frequencies."""
-    return (None, 0) if inv_freq is None else (_arg(inv_freq, name, torch.float64, (None,), dev), 2 * inv_freq.numel())
+    if inv_freq is None:
+        return None, 0
+    n = inv_freq.numel()
+    return _arg(inv_freq, name, _F64, (n,), dev), 2 * n
 
 
 def _weight(w, name: str, d: int, dev: int):
-    return None if w is None else _arg(w, name, torch.bfloat16, (d,), dev)
+    return None if w is None else _arg(w, name, _BF16, (d,), dev)
 
 
 def _token_map(T: int, positions, cu_seqlens_q, seqlens_k, dev: int):
     """(positions, cu_seqlens_q, seqlens_k, batch) as the library takes them."""
     B = 1 if cu_seqlens_q is None else cu_seqlens_q.numel() - 1
-    return (None if positions is None else _arg(positions, "positions", torch.int32, (T,), dev),
-            None if cu_seqlens_q is None else _arg(cu_seqlens_q, "cu_seqlens_q", torch.int32, (None,), dev),
-            None if seqlens_k is None else _arg(seqlens_k, "seqlens_k", torch.int32, (B,), dev), B)
+    return (None if positions is None else _arg(positions, "positions", _I32, (T,), dev),
+            None if cu_seqlens_q is None else _arg(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev),
+            None if seqlens_k is None else _arg(seqlens_k, "seqlens_k", _I32, (B,), dev), B)
 
 
 def norm_rope(Q, K=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, cu_seqlens_q=None, seqlens_k=None,
@@ -458,19 +471,19 @@ def norm_rope(Q, K=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     themselves among them; rows outside the sequences are left as they were (see dsa_norm_rope)."""
     T, Hq, d = Q.shape
     dev = Q.get_device()
-    q, qs = _rows(Q, "Q", (T, Hq, d), dev)
+    q, qs = _rows(Q, "Q", T, Hq, d, dev)
     Hk, k, ks = 0, None, 0
     if K is not None:
         Hk = K.shape[1]
-        k, ks = _rows(K, "K", (T, Hk, d), dev)
+        k, ks = _rows(K, "K", T, Hk, d, dev)
     if out is not None:
         Qo, Ko = out
-        qo, qos = _rows(Qo, "Q out", (T, Hq, d), dev)
+        qo, qos = _rows(Qo, "Q out", T, Hq, d, dev)
     else:
-        Qo = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=Q.device)
-        Ko = None if K is None else torch.empty((T, Hk, d), dtype=torch.bfloat16, device=Q.device)
+        Qo = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        Ko = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
         qo, qos = Qo.data_ptr(), Hq * d
-    ko, kos = (None, 0) if K is None else _rows(Ko, "K out", (T, Hk, d), dev)
+    ko, kos = (None, 0) if K is None else _rows(Ko, "K out", T, Hk, d, dev)
     pos, cu, lens, B = _token_map(T, positions, cu_seqlens_q, seqlens_k, dev)
     freq, rotary = _rope(inv_freq, "inv_freq", dev)
     gq = _weight(q_weight, "q_weight", d, dev)
@@ -494,20 +507,20 @@ def norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight=None, k_weight=None, inv_freq=N
     write, dQ_out and dK_out themselves among them (see dsa_norm_rope_bwd)."""
     T, Hq, d = Q.shape
     dev = Q.get_device()
-    q, qs = _rows(Q, "Q", (T, Hq, d), dev)
-    dqo, dqos = _rows(dQ_out, "dQ_out", (T, Hq, d), dev)
+    q, qs = _rows(Q, "Q", T, Hq, d, dev)
+    dqo, dqos = _rows(dQ_out, "dQ_out", T, Hq, d, dev)
     Hk, k, ks, dko, dkos = 0, None, 0, None, 0
     if K is not None:
         Hk = K.shape[1]
-        k, ks = _rows(K, "K", (T, Hk, d), dev)
-        dko, dkos = _rows(dK_out, "dK_out", (T, Hk, d), dev)
+        k, ks = _rows(K, "K", T, Hk, d, dev)
+        dko, dkos = _rows(dK_out, "dK_out", T, Hk, d, dev)
     if out is not None:
         dQ, dK = out
     else:
-        dQ = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=Q.device)
-        dK = None if K is None else torch.empty((T, Hk, d), dtype=torch.bfloat16, device=Q.device)
-    dq, dqs = _rows(dQ, "dQ", (T, Hq, d), dev)
-    dk, dks = (None, 0) if K is None else _rows(dK, "dK", (T, Hk, d), dev)
+        dQ = torch.empty_like(Q, memory_format=torch.contiguous_format)
+        dK = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
+    dq, dqs = _rows(dQ, "dQ", T, Hq, d, dev)
+    dk, dks = (None, 0) if K is None else _rows(dK, "dK", T, Hk, d, dev)
     pos, cu, lens, B = _token_map(T, positions, cu_seqlens_q, seqlens_k, dev)
     freq, rotary = _rope(inv_freq, "inv_freq", dev)
     gq = _weight(q_weight, "q_weight", d, dev)
@@ -516,8 +529,8 @@ def norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight=None, k_weight=None, inv_freq=N
     dgk = None if gk is None else torch.empty(d, dtype=torch.float32, device=Q.device)
     if T == 0:
         return dQ, dK, None if dgq is None else dgq.zero_(), None if dgk is None else dgk.zero_()
-    if workspace is None and (gq is not None or gk is not None):
-        workspace = torch.empty(max(norm_rope_bwd_workspace_bytes(T, Hq, Hk, d), 16), dtype=torch.uint8, device=Q.device)
+    if gq is not None or gk is not None:
+        workspace = _workspace(workspace, norm_rope_bwd_workspace_bytes(T, Hq, Hk, d), Q.device, dev)
     _launch(dev, "dsa_norm_rope_bwd", q, qs, k, ks, dqo, dqos, dko, dkos, gq, gk, eps, freq, rotary, interleaved, pos, cu,
             lens, B, T, Hq, Hk, d, dq, dqs, dk, dks, _ptr(dgq), _ptr(dgk), _ptr(workspace),
             0 if workspace is None else workspace.numel())
@@ -527,8 +540,8 @@ def norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight=None, k_weight=None, inv_freq=N
 def _table(block_table, seqlens_k, dev: int):
     """(block_table, max_pages, seqlens_k, batch) as the library takes them."""
     B, width = block_table.shape
-    return (_arg(block_table, "block_table", torch.int32, (B, width), dev), width,
-            _arg(seqlens_k, "seqlens_k", torch.int32, (B,), dev), B)
+    return (_arg(block_table, "block_table", _I32, (B, width), dev), width,
+            _arg(seqlens_k, "seqlens_k", _I32, (B,), dev), B)
 
 
 def cache_append(K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, cu_seqlens_q, seqlens_k, k_weight=None,
@@ -542,8 +555,8 @@ def cache_append(K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, cu_seq
     last one sits at seqlens_k - 1.  Tokens without a page are dropped (see dsa_cache_append)."""
     T, Hkv, d = K.shape
     dev = K.get_device()
-    k, ks = _rows(K, "K", (T, Hkv, d), dev)
-    v, vs = _rows(V, "V", (T, Hkv, d), dev)
+    k, ks = _rows(K, "K", T, Hkv, d, dev)
+    v, vs = _rows(V, "V", T, Hkv, d, dev)
     table, width, lens, B = _table(block_table, seqlens_k, dev)
     pages, page = k_cache.shape[:2]
     kc, kcs = _pool(k_cache, "k_cache", (pages, page, Hkv, d), dev)
@@ -551,7 +564,7 @@ def cache_append(K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, cu_seq
     d_I, i, is_, ic, ics = 0, None, 0, None, 0
     if k_idx is not None:
         d_I = k_idx.shape[1]
-        i, is_ = _rows(k_idx, "k_idx", (T, d_I), dev)
+        i, is_ = _flat_rows(k_idx, "k_idx", T, d_I, dev)
         ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
     freq, rotary = _rope(inv_freq, "inv_freq", dev)
     ifreq, irotary = (None, 0) if k_idx is None else _rope(idx_inv_freq, "idx_inv_freq", dev)
@@ -577,9 +590,9 @@ def index_paged(q_idx, k_idx_cache, w, block_table, seqlens_k, max_seqlen_k: int
     ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
     if scores is None:
         scores = torch.full((B, _ld(max_seqlen_k)), float("-inf"), dtype=torch.float32, device=q_idx.device)
-    out = _arg(scores, "scores", torch.float32, (B, None), dev)
-    _launch(dev, "dsa_index_paged", _arg(q_idx, "q_idx", torch.bfloat16, (block_table.shape[0], H_I, d_I), dev), ic, ics,
-            _arg(w, "w", torch.bfloat16, (B, H_I), dev), table, width, lens, B, pages, page, max_seqlen_k, H_I, d_I, out,
+    out = _arg(scores, "scores", _F32, (B, scores.shape[1]), dev)
+    _launch(dev, "dsa_index_paged", _arg(q_idx, "q_idx", _BF16, (block_table.shape[0], H_I, d_I), dev), ic, ics,
+            _arg(w, "w", _BF16, (B, H_I), dev), table, width, lens, B, pages, page, max_seqlen_k, H_I, d_I, out,
             scores.shape[1])
     return scores
 
@@ -596,14 +609,14 @@ def sparse_attn_decode_paged(Q, k_cache, v_cache, indices, block_table, seqlens_
     vc, vcs = _pool(v_cache, "v_cache", (pages, page, Hkv, d), dev)
     if out is not None:
         O, lse = out
-        _arg(O, "O", torch.bfloat16, (B, Hq, d), dev)
+        _arg(O, "O", _BF16, (B, Hq, d), dev)
         if lse is not None:
-            _arg(lse, "lse", torch.float32, (B, Hq), dev)
+            _arg(lse, "lse", _F32, (B, Hq), dev)
     else:
-        O = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=Q.device)
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=Q.device)
-    _launch(dev, "dsa_sparse_attn_decode_paged", _arg(Q, "Q", torch.bfloat16, (block_table.shape[0], Hq, d), dev), kc, kcs,
-            vc, vcs, _arg(indices, "indices", torch.int32, (B, None), dev), table, width, lens, B, pages, page, Hq, Hkv, d,
+        O = torch.empty_like(Q)
+        lse = torch.empty((B, Hq), dtype=_F32, device=Q.device)
+    _launch(dev, "dsa_sparse_attn_decode_paged", _arg(Q, "Q", _BF16, (block_table.shape[0], Hq, d), dev), kc, kcs,
+            vc, vcs, _arg(indices, "indices", _I32, (B, indices.shape[1]), dev), table, width, lens, B, pages, page, Hq, Hkv, d,
             indices.shape[1], 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(), _ptr(lse))
     return O, lse
 
@@ -614,21 +627,21 @@ def decode_paged_workspace_bytes(batch: int, max_seqlen_k: int) -> int:
 
 def _decode_out(out, B: int, k: int, Hq: int, d: int, device, dev: int):
     if out is None:
-        return (torch.empty((B, k), dtype=torch.int32, device=device),
+        return (torch.empty((B, k), dtype=_I32, device=device),
                 torch.empty((B, Hq, d), dtype=torch.bfloat16, device=device),
                 torch.empty((B, Hq), dtype=torch.float32, device=device))
     indices, O, lse = out
-    _arg(indices, "indices", torch.int32, (B, k), dev)
-    _arg(O, "O", torch.bfloat16, (B, Hq, d), dev)
+    _arg(indices, "indices", _I32, (B, k), dev)
+    _arg(O, "O", _BF16, (B, Hq, d), dev)
     if lse is not None:
-        _arg(lse, "lse", torch.float32, (B, Hq), dev)
+        _arg(lse, "lse", _F32, (B, Hq), dev)
     return out
 
 
 def _workspace(workspace, nbytes: int, device, dev: int):
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _arg(workspace, "workspace", torch.uint8, (None,), dev)
+    _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     return workspace
 
 
@@ -646,8 +659,8 @@ def decode_paged(q_idx, w, Q, k_cache, v_cache, k_idx_cache, block_table, seqlen
     ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
     ws = _workspace(workspace, decode_paged_workspace_bytes(B, max_seqlen_k), Q.device, dev)
     indices, O, lse = out = _decode_out(out, B, k, Hq, d, Q.device, dev)
-    _launch(dev, "dsa_decode_paged", _arg(q_idx, "q_idx", torch.bfloat16, (B, H_I, d_I), dev),
-            _arg(w, "w", torch.bfloat16, (B, H_I), dev), _arg(Q, "Q", torch.bfloat16, (block_table.shape[0], Hq, d), dev),
+    _launch(dev, "dsa_decode_paged", _arg(q_idx, "q_idx", _BF16, (B, H_I, d_I), dev),
+            _arg(w, "w", _BF16, (B, H_I), dev), _arg(Q, "Q", _BF16, (block_table.shape[0], Hq, d), dev),
             kc, kcs, vc, vcs, ic, ics, table, width, lens, B, pages, page, max_seqlen_k, Hq, Hkv, d, H_I, d_I, k,
             1.0 / math.sqrt(d) if scale is None else scale, indices.data_ptr(), O.data_ptr(), _ptr(lse), ws.data_ptr(),
             ws.numel())
@@ -681,13 +694,13 @@ def decode_step_paged(q_idx, w, Q, K, V, k_idx, k_cache, v_cache, k_idx_cache, b
     ifreq, irotary = _rope(idx_inv_freq, "idx_inv_freq", dev)
     ws = _workspace(workspace, decode_step_paged_workspace_bytes(B, max_seqlen_k, Hq, d, H_I, d_I), Q.device, dev)
     indices, O, lse = out = _decode_out(out, B, k, Hq, d, Q.device, dev)
-    _launch(dev, "dsa_decode_step_paged", *_rows(q_idx, "q_idx", (B, H_I, d_I), dev),
-            _arg(w, "w", torch.bfloat16, (B, H_I), dev), *_rows(Q, "Q", (B, Hq, d), dev), *_rows(K, "K", (B, Hkv, d), dev),
-            *_rows(V, "V", (B, Hkv, d), dev), *_rows(k_idx, "k_idx", (B, d_I), dev),
+    _launch(dev, "dsa_decode_step_paged", *_rows(q_idx, "q_idx", B, H_I, d_I, dev),
+            _arg(w, "w", _BF16, (B, H_I), dev), *_rows(Q, "Q", B, Hq, d, dev), *_rows(K, "K", B, Hkv, d, dev),
+            *_rows(V, "V", B, Hkv, d, dev), *_flat_rows(k_idx, "k_idx", B, d_I, dev),
             _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev),
             _weight(q_idx_weight, "q_idx_weight", d_I, dev), _weight(k_idx_weight, "k_idx_weight", d_I, dev), eps, freq,
             rotary, interleaved, ifreq, irotary, idx_interleaved,
-            None if positions is None else _arg(positions, "positions", torch.int32, (B,), dev), kc, kcs, vc, vcs, ic, ics,
+            None if positions is None else _arg(positions, "positions", _I32, (B,), dev), kc, kcs, vc, vcs, ic, ics,
             table, width, lens, B, pages, page, max_seqlen_k, Hq, Hkv, d, H_I, d_I, k,
             1.0 / math.sqrt(d) if scale is None else scale, indices.data_ptr(), O.data_ptr(), _ptr(lse), ws.data_ptr(),
             ws.numel())
