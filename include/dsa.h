@@ -452,7 +452,8 @@ DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t 
  * (7b) Decode attention over the paged cache: (4) with its positions looked up in the
  * table.  Entries of indices outside [0, length) or on a page that is not there are ignored;
  * an empty set gives O = 0 and lse = -inf.  One launch and no workspace.  Two equal entries
- * of a row count twice, as in (3).
+ * of a row count twice, as in (3).  Repeats of a call are bit-identical; how a row's slots are
+ * split over blocks depends on the batch, so a row's last bits may differ between batches.
  * Supported: the shapes of (4).
  * ------------------------------------------------------------------------------- */
 DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int64_t k_page_stride,

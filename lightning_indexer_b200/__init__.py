@@ -480,8 +480,8 @@ def norm_rope(Q, K=None, q_weight=None, k_weight=None, inv_freq=None, positions=
         Qo, Ko = out
         qo, qos = _rows(Qo, "Q out", T, Hq, d, dev)
     else:
-        Qo = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        Ko = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
+        Qo = torch.empty_like(Q)
+        Ko = None if K is None else torch.empty_like(K)
         qo, qos = Qo.data_ptr(), Hq * d
     ko, kos = (None, 0) if K is None else _rows(Ko, "K out", T, Hk, d, dev)
     pos, cu, lens, B = _token_map(T, positions, cu_seqlens_q, seqlens_k, dev)
@@ -517,8 +517,8 @@ def norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight=None, k_weight=None, inv_freq=N
     if out is not None:
         dQ, dK = out
     else:
-        dQ = torch.empty_like(Q, memory_format=torch.contiguous_format)
-        dK = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
+        dQ = torch.empty_like(Q)
+        dK = None if K is None else torch.empty_like(K)
     dq, dqs = _rows(dQ, "dQ", T, Hq, d, dev)
     dk, dks = (None, 0) if K is None else _rows(dK, "dK", T, Hk, d, dev)
     pos, cu, lens, B = _token_map(T, positions, cu_seqlens_q, seqlens_k, dev)

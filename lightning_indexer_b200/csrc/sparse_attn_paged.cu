@@ -9,10 +9,11 @@
 // The work is a gather of 2 Hkv d bf16 per selected position; the products are 16 operations
 // per byte, so warp-level MMA carries them (16 keys x 8 heads, no padding) as in the gather
 // kernel of the contiguous cache.  One launch and no scratch memory: the selected slots of a
-// (row, KV head) are dealt in chunks of 16 to the warps of a thread-block cluster, each warp
-// runs one online softmax over its chunks, and the partial (max, sum, O) of the warps are
-// joined in shared memory, then over the cluster through distributed shared memory, always in
-// the same order.
+// (row, KV head) are dealt 32 at a time to the warps of a thread-block cluster, each warp runs
+// one online softmax over its slots, 16 at a time, and the partial (max, sum, O) of the warps
+// are joined in shared memory, then over the cluster: each block sends its share of every
+// output to the block that finishes it (remote stores, one barrier, local sums), always summed
+// in the same order.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -36,14 +37,18 @@ struct SAPagedParams {
   float* lse;   // [rows, Hq] or null
 };
 
+constexpr int SAP_MAX_SPLITS = 8;  // blocks of a cluster (the portable limit)
+
 template <int D, int WARPS, int STAGES>
 struct SAPagedSmem {
   static constexpr int STAGE_BYTES = 2 * 16 * D * 2;  // K and V rows of a chunk
   static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
   static constexpr int OFF_ML = RING;                    // [WARPS][8] float4: max, sum, rounded sum
-  static constexpr int OFF_CO = OFF_ML + WARPS * 8 * 16;  // [8][D] the block's O
-  static constexpr int OFF_CML = OFF_CO + 8 * D * 4;      // [8] float4
-  static constexpr int BYTES = OFF_CML + 8 * 16;
+  // what the cluster's blocks send to this one: the states of all of them, and their O of the
+  // outputs that this block finishes (outputs rank, rank + splits, ... of the 8 D)
+  static constexpr int OFF_CML = OFF_ML + WARPS * 8 * 16;             // [splits][8] float4
+  static constexpr int OFF_CO = OFF_CML + SAP_MAX_SPLITS * 8 * 16;    // [splits][ceil(8 D / splits)]
+  static constexpr int BYTES = OFF_CO + (8 * D + SAP_MAX_SPLITS) * 4;
   static_assert(STAGES * STAGE_BYTES >= 8 * D * 4, "a warp's O replaces its ring");
 };
 
@@ -55,6 +60,7 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   constexpr int TILE_BYTES = C::STAGE_BYTES / 2;
   pdl_wait();
   pdl_trigger();
+  if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint8_t* my = smem + warp * STAGES * C::STAGE_BYTES;
@@ -63,14 +69,15 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   const int g = cid % p.Hkv;
   const long long row = cid / p.Hkv;
 
-  const int len = __ldg(p.lens + row);
   const int* idx = p.indices + row * p.k;
   const int* trow = p.table + row * p.table_width;
-  const int nchunks = p.k / 16, step = splits * WARPS, c0 = rank * WARPS + warp;
+  const int nunits = (p.k + 31) / 32, step = splits * WARPS, u0 = rank * WARPS + warp;
+  const int nchunks = u0 < nunits ? 2 * ((nunits - 1 - u0) / step + 1) : 0;  // of this warp
   const int kv_row = p.Hkv * D;
   const uint16_t* Kg = p.K + g * D;
   const uint16_t* Vg = p.V + g * D;
 
+  const int len = __ldg(p.lens + row);
   uint32_t qb[MT][2];
   {
     const int head = lane / 4;
@@ -83,9 +90,11 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
     }
   }
 
-  // cache slot (page * P + row in page) of the position in this lane's slot of chunk c, or -1
-  const int slot = lane & 15;
-  auto position = [&](int c) { return c < nchunks ? __ldg(idx + c * 16 + slot) : -1; };
+  // Slots are handled 32 at a time, a unit, one per lane: two chunks.  The chain position ->
+  // page -> row is three dependent loads, so a unit's pages are looked up one unit ahead of its
+  // copies and its positions two ahead.
+  auto position = [&](int u) { return u < nunits && u * 32 + lane < p.k ? __ldg(idx + u * 32 + lane) : -1; };
+  // cache slot (page * P + row in page) of a position, or -1
   auto cache_slot = [&](int s) {
     if ((unsigned)s >= (unsigned)max(len, 0)) return -1;
     const int pg = s >> p.page_shift;
@@ -94,14 +103,14 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
     if ((unsigned)page >= (unsigned)p.num_pages) return -1;
     return (page << p.page_shift) | (s & ((1 << p.page_shift) - 1));
   };
-  // starts the copies of a chunk whose slots the lanes hold; returns its mask of valid slots
-  auto issue = [&](int st, int mine) -> uint32_t {
+  // starts the copies of a chunk, the lanes' slots from `first` on; returns its mask of valid slots
+  auto issue = [&](int st, int mine, int first) -> uint32_t {
     const uint32_t kdst = my_s + st * C::STAGE_BYTES, vdst = kdst + TILE_BYTES;
     const int sub = lane >> 3, c = lane & 7;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = 4 * j + sub;
-      const int cs = __shfl_sync(0xffffffffu, mine, r);
+      const int cs = __shfl_sync(0xffffffffu, mine, first + r);
       const bool valid = cs >= 0;
       const int page = cs >> p.page_shift;
       const int in = (cs & ((1 << p.page_shift) - 1)) * kv_row + c * 8;
@@ -115,7 +124,7 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
       }
     }
     cp_async_commit();
-    return __ballot_sync(0xffffffffu, mine >= 0) & 0xFFFFu;
+    return (__ballot_sync(0xffffffffu, mine >= 0) >> first) & 0xFFFFu;
   };
 
   float acc[MT][4] = {};
@@ -124,28 +133,32 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   float r0 = 0.f, r1 = 0.f;              // the same of the bf16-rounded weights that multiply V
 
   uint32_t vmr[STAGES];  // valid masks of the chunks in flight, the next one to use first
-  int s_next = position(c0), cs_next = -1;  // positions one chunk ahead of the slots
-  cs_next = cache_slot(s_next);
-  s_next = position(c0 + step);
-#pragma unroll
-  for (int j = 0; j < STAGES - 1; ++j) {
-    const int cur = cs_next;
-    cs_next = cache_slot(s_next);
-    s_next = position(c0 + (j + 2) * step);
-    vmr[j] = c0 + j * step < nchunks ? issue(j, cur) : (cp_async_commit(), 0u);
+  int cs_cur = -1, cs_next, s_next, u_next = u0 + step;
+  {
+    const int s0 = position(u0), s1 = position(u_next);
+    cs_cur = cache_slot(s0);
+    cs_next = cache_slot(s1);
+    s_next = position(u_next += step);
   }
-
-  int n = 0;
-#pragma unroll 1
-  for (int c = c0; c < nchunks; c += step, ++n) {
-    const int st = n % STAGES;
-    {
-      const int cn = c + (STAGES - 1) * step;
-      const int cur = cs_next;
-      cs_next = cache_slot(s_next);
-      s_next = position(cn + 2 * step);
-      vmr[STAGES - 1] = cn < nchunks ? issue((n + STAGES - 1) % STAGES, cur) : (cp_async_commit(), 0u);
+  auto issue_chunk = [&](int n) -> uint32_t {
+    if (n >= nchunks) {
+      cp_async_commit();
+      return 0u;
     }
+    if (n > 0 && n % 2 == 0) {  // the next unit
+      cs_cur = cs_next;
+      cs_next = cache_slot(s_next);
+      s_next = position(u_next += step);
+    }
+    return issue(n % STAGES, cs_cur, n % 2 * 16);
+  };
+#pragma unroll
+  for (int j = 0; j < STAGES - 1; ++j) vmr[j] = issue_chunk(j);
+
+#pragma unroll 1
+  for (int n = 0; n < nchunks; ++n) {
+    const int st = n % STAGES;
+    vmr[STAGES - 1] = issue_chunk(n + STAGES - 1);
     cp_async_wait<STAGES - 1>();
     __syncwarp();
     const uint32_t vm = vmr[0];
@@ -242,9 +255,13 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   }
   __syncthreads();
 
-  // ---- the block's state
+  // ---- the block's state, sent to the blocks that finish the outputs: output e belongs to
+  // block e % splits.  Every block of the cluster has started (the barrier's first phase).
+  cg::cluster_group cluster = cg::this_cluster();
   float* s_co = reinterpret_cast<float*>(smem + C::OFF_CO);
   float4* s_cml = reinterpret_cast<float4*>(smem + C::OFF_CML);
+  const int share = (8 * D + splits - 1) / splits;
+  if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int e = threadIdx.x; e < p.G * D; e += WARPS * 32) {
     const int h = e / D;
     float M = -INFINITY;
@@ -260,40 +277,51 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
       R = fmaf(ml.z, f, R);
       o = fmaf(reinterpret_cast<const float*>(smem + w * STAGES * C::STAGE_BYTES)[e], f, o);
     }
-    s_co[e] = o;
-    if (e % D == 0) s_cml[h] = make_float4(M, L, R, 0.f);
+    if (splits == 1) {
+      const long long head = row * p.Hq + g * p.G + h;
+      p.O[head * D + e % D] = __bfloat16_as_ushort(__float2bfloat16_rn(R > 0.f ? o / R : 0.f));
+      if (p.lse && e % D == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+    } else {
+      cluster.map_shared_rank(s_co, e % splits)[rank * share + e / splits] = o;
+      if (e % D < splits) cluster.map_shared_rank(s_cml, e % D)[rank * 8 + h] = make_float4(M, L, R, 0.f);
+    }
   }
+  if (splits == 1) return;  // block-uniform
 
-  // ---- over the cluster: each block finishes a share of the (head, dim) outputs
-  cg::cluster_group cluster = cg::this_cluster();
-  if (splits > 1) cluster.sync(); else __syncthreads();
-  for (int e = rank * WARPS * 32 + threadIdx.x; e < p.G * D; e += splits * WARPS * 32) {
+  // ---- over the cluster: this block's outputs from every block's share, in order
+  cluster.sync();
+  for (int e = rank + threadIdx.x * splits; e < p.G * D; e += WARPS * 32 * splits) {
     const int h = e / D;
-    float M = -INFINITY;
-    for (int q = 0; q < splits; ++q) M = fmaxf(M, (splits > 1 ? cluster.map_shared_rank(s_cml, q) : s_cml)[h].x);
+    float m[SAP_MAX_SPLITS], M = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < SAP_MAX_SPLITS; ++q) {
+      m[q] = q < splits ? s_cml[q * 8 + h].x : -INFINITY;
+      M = fmaxf(M, m[q]);
+    }
     const float mu = M == -INFINITY ? 0.f : M;
     float o = 0.f, L = 0.f, R = 0.f;
-    for (int q = 0; q < splits; ++q) {
-      const float4 ml = (splits > 1 ? cluster.map_shared_rank(s_cml, q) : s_cml)[h];
-      const float f = exp2f(ml.x - mu);
+#pragma unroll
+    for (int q = 0; q < SAP_MAX_SPLITS; ++q) {
+      if (q >= splits) continue;
+      const float4 ml = s_cml[q * 8 + h];
+      const float f = exp2f(m[q] - mu);
       L = fmaf(ml.y, f, L);
       R = fmaf(ml.z, f, R);
-      o = fmaf((splits > 1 ? cluster.map_shared_rank(s_co, q) : s_co)[e], f, o);
+      o = fmaf(s_co[q * share + e / splits], f, o);
     }
     const long long head = row * p.Hq + g * p.G + h;
     p.O[head * D + e % D] = __bfloat16_as_ushort(__float2bfloat16_rn(R > 0.f ? o / R : 0.f));
     if (p.lse && e % D == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
   }
-  if (splits > 1) cluster.sync();  // the other blocks may still read this one's state
 }
 
 }  // namespace dsa
 
 namespace dsa_host {
 
-template <int D>
-static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, cudaStream_t stream) {
-  constexpr int WARPS = 4, STAGES = 2;
+template <int D, int WARPS>
+static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int splits, bool pdl, cudaStream_t stream) {
+  constexpr int STAGES = 2;
   auto kern = dsa::sparse_attn_paged_kernel<D, WARPS, STAGES>;
   const int smem = dsa::SAPagedSmem<D, WARPS, STAGES>::BYTES;
   static DeviceFlag done;
@@ -303,9 +331,6 @@ static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, c
     if (e_ != cudaSuccess) return cuda_fail(e_);
     done = true;
   }
-  const long long groups = (long long)batch * p.Hkv;
-  int splits = std::min(8, std::max(1, p.k / (16 * WARPS)));
-  while (splits > 1 && groups * splits > 0x7FFFFFFFLL) --splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * splits));
   cfg.blockDim = dim3(WARPS * 32);
@@ -322,6 +347,22 @@ static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, c
   cfg.numAttrs = pdl ? 2 : 1;
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, splits); e != cudaSuccess) return cuda_fail(e);
   return last_launch_status();
+}
+
+// While the (row, KV head) groups do not fill the SMs, blocks of 8 warps, one per SM, and the
+// largest cluster that still gives every block an SM of its own and every warp a unit; past
+// that, blocks of 4 warps without clusters.  Joining over a cluster costs about 2.5 us and a
+// block's start as much again, so more and smaller pieces lose: 16 sequences of 2048 slots
+// (64 groups) take 19.5 us as clusters of 2, 29 as clusters of 8; 64 sequences 48 us unsplit
+// with 4 warps, 53 with 8, 58 as clusters of 2.
+template <int D>
+static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, cudaStream_t stream) {
+  const long long groups = (long long)batch * p.Hkv;
+  const int sms = sm_count();
+  if (groups > sms) return sa_paged_launch_t<D, 4>(p, groups, 1, pdl, stream);
+  int splits = 1;
+  while (splits < dsa::SAP_MAX_SPLITS && groups * splits * 2 <= sms && splits * 2 * 8 * 32 <= p.k) splits *= 2;
+  return sa_paged_launch_t<D, 8>(p, groups, splits, pdl, stream);
 }
 
 int sparse_attn_paged_launch(const dsa::SAPagedParams& p, int batch, int d, bool pdl, cudaStream_t stream) {

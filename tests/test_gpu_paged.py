@@ -234,10 +234,30 @@ def test_attention_paged(Hq, Hkv, d, k, page):
         assert bool(((ref.f64(O[b]) - want).abs() <= bound).all()), (b, n)
         assert torch.equal(torch.isinf(wlse), torch.isinf(lse[b].cpu()))
         assert n == 0 or float((ref.f64(lse[b]) - wlse).abs().max()) <= LSE_ATOL
-    # one row alone, without the lse, and again: the same bits
+    # again: the same bits; one row alone, without the lse, is split differently and meets the same bound
+    again = dsa.sparse_attn_decode_paged(Q.cuda(), kc.cuda(), vc.cuda(), idx.cuda(), table.cuda(), i32(lens).cuda())
+    assert torch.equal(again[0], O) and torch.equal(again[1], lse)
     one = torch.empty(1, Hq, d, dtype=BF16, device="cuda")
     dsa.sparse_attn_decode_paged(Q[4:5].cuda(), kc.cuda(), vc.cuda(), idx[4:5].cuda(), table[4:5].cuda(), i32(lens[4:5]).cuda(), out=(one, None))
-    assert torch.equal(one[0], O[4])
+    s = idx[4][idx[4] >= 0].long()
+    at = table[4].long()[s // page], s % page
+    want, _, bound = attention(ref.f64(Q[4]), ref.f64(kc[at]), ref.f64(vc[at]), d ** -0.5)
+    assert bool(((ref.f64(one[0]) - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("B", [9, 36, 150])
+def test_attention_paged_batches(B):
+    """Batches on both sides of the split rule, every row against its bound."""
+    page, d, k = 32, 64, 512
+    lens = [(97 * b) % 1500 for b in range(B)]
+    Q, kc, vc, idx, table, _ = make_attention_case(8, 2, d, k, page, lens, B)
+    O, lse = dsa.sparse_attn_decode_paged(Q.cuda(), kc.cuda(), vc.cuda(), idx.cuda(), table.cuda(), i32(lens).cuda())
+    for b, n in enumerate(lens):
+        s = idx[b][idx[b] >= 0].long()
+        at = table[b].long()[s // page], s % page
+        want, wlse, bound = attention(ref.f64(Q[b]), ref.f64(kc[at]), ref.f64(vc[at]), d ** -0.5)
+        assert bool(((ref.f64(O[b]) - want).abs() <= bound).all()), (b, n)
+        assert n == 0 or float((ref.f64(lse[b]) - wlse).abs().max()) <= LSE_ATOL
 
 
 def test_attention_ignores_what_is_not_there():
