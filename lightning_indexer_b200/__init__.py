@@ -372,91 +372,24 @@ def indexer_kl_loss_sparse(Q, K, q_idx, k_idx, w, indices, cu_seqlens_q, cu_seql
     return loss, kl, dq, dk, dw
 
 
-# ---- head norm and rotation, and the paged cache.  Sizes that the library cannot see in a
-# pointer (rows, tables, pages) are checked here against one another; the work is enqueued on
-# the tensors' own device, on its current stream.
+# ---- head norm and rotation, and the paged cache.  These are the calls of a decode step, whose
+# kernels take a few microseconds: their checks and marshalling are native (csrc/binding.cpp).
+# Sizes that the library cannot see in a pointer (rows, tables, pages) are checked there against
+# one another (ValueError), and the work is enqueued on the tensors' own device, on its current
+# stream.
 
-_BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the handle alone: current_stream() costs 3 us of a decode step's call
-
-
-def _refuse(t: torch.Tensor, name: str, dtype, shape, dev: int, what: str):
-    """Says why a tensor is refused: the checks themselves are one expression each, for speed."""
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must have {what}")
+_native_module = None
 
 
-def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int):
-    """Pointer of a contiguous tensor of this type, shape and device."""
-    if t.dtype is dtype and t.get_device() == dev >= 0 and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
-    _refuse(t, name, dtype, shape, dev, "contiguous elements")
-
-
-def _rows(t: torch.Tensor, name: str, T: int, heads: int, d: int, dev: int):
-    """(pointer, token stride) of bf16 rows [T, heads, d] whose heads are dense."""
-    if t.dtype is _BF16 and t.get_device() == dev >= 0 and t.shape == (T, heads, d):
-        s0, s1, s2 = t.stride()
-        if s2 == 1 and (s1 == d or heads == 1):
-            return t.data_ptr(), (s0 if T > 1 else heads * d)
-    _refuse(t, name, _BF16, (T, heads, d), dev, "dense heads (only the token stride may be larger)")
-
-
-def _flat_rows(t: torch.Tensor, name: str, T: int, d: int, dev: int):
-    """(pointer, token stride) of bf16 rows [T, d]."""
-    if t.dtype is _BF16 and t.get_device() == dev >= 0 and t.shape == (T, d):
-        s0, s1 = t.stride()
-        if s1 == 1:
-            return t.data_ptr(), (s0 if T > 1 else d)
-    _refuse(t, name, _BF16, (T, d), dev, "dense rows (only the token stride may be larger)")
-
-
-def _pool(t: torch.Tensor, name: str, shape, dev: int):
-    """(pointer, page stride) of a bf16 cache [pages, page_size, ...] whose pages are dense."""
-    if t.dtype is _BF16 and t.get_device() == dev >= 0 and t.shape == shape:
-        st, dense, ok = t.stride(), 1, True
-        for i in range(len(shape) - 1, 0, -1):
-            ok = ok and (st[i] == dense or shape[i] == 1)
-            dense *= shape[i]
-        if ok:
-            return t.data_ptr(), (st[0] if shape[0] > 1 else dense)
-    _refuse(t, name, _BF16, shape, dev, "dense pages (only the page stride may be larger)")
-
-
-def _launch(dev: int, name: str, *args):
-    """Calls an entry point with the current stream of device `dev` as its last argument."""
-    if dev == torch.cuda.current_device():
-        st = getattr(_lib.load(), name)(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = getattr(_lib.load(), name)(*args, _raw_stream(dev))
-    if st != 0:
-        raise DSAError(name, st)
-
-
-def _rope(inv_freq, name: str, dev: int):
-    """(pointer, rotary_dim) of the frequencies."""
-    if inv_freq is None:
-        return None, 0
-    n = inv_freq.numel()
-    return _arg(inv_freq, name, _F64, (n,), dev), 2 * n
-
-
-def _weight(w, name: str, d: int, dev: int):
-    return None if w is None else _arg(w, name, _BF16, (d,), dev)
-
-
-def _token_map(T: int, positions, cu_seqlens_q, seqlens_k, dev: int):
-    """(positions, cu_seqlens_q, seqlens_k, batch) as the library takes them."""
-    B = 1 if cu_seqlens_q is None else cu_seqlens_q.numel() - 1
-    return (None if positions is None else _arg(positions, "positions", _I32, (T,), dev),
-            None if cu_seqlens_q is None else _arg(cu_seqlens_q, "cu_seqlens_q", _I32, (B + 1,), dev),
-            None if seqlens_k is None else _arg(seqlens_k, "seqlens_k", _I32, (B,), dev), B)
+def _native():
+    """The native binding, loaded on first use.  Raises ImportError if it or the library is missing."""
+    global _native_module
+    if _native_module is None:
+        _lib.load()
+        from . import _binding
+        _binding.set_errors(DSAError, torch.cuda.OutOfMemoryError)
+        _native_module = _binding
+    return _native_module
 
 
 def norm_rope(Q, K=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, cu_seqlens_q=None, seqlens_k=None,
@@ -469,30 +402,7 @@ def norm_rope(Q, K=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     token's position is its index in its sequence of cu_seqlens_q, shifted so that the last one
     sits at seqlens_k - 1 where that is given.  `out` may give (Q', K') to write, the inputs
     themselves among them; rows outside the sequences are left as they were (see dsa_norm_rope)."""
-    T, Hq, d = Q.shape
-    dev = Q.get_device()
-    q, qs = _rows(Q, "Q", T, Hq, d, dev)
-    Hk, k, ks = 0, None, 0
-    if K is not None:
-        Hk = K.shape[1]
-        k, ks = _rows(K, "K", T, Hk, d, dev)
-    if out is not None:
-        Qo, Ko = out
-        qo, qos = _rows(Qo, "Q out", T, Hq, d, dev)
-    else:
-        Qo = torch.empty_like(Q)
-        Ko = None if K is None else torch.empty_like(K)
-        qo, qos = Qo.data_ptr(), Hq * d
-    ko, kos = (None, 0) if K is None else _rows(Ko, "K out", T, Hk, d, dev)
-    pos, cu, lens, B = _token_map(T, positions, cu_seqlens_q, seqlens_k, dev)
-    freq, rotary = _rope(inv_freq, "inv_freq", dev)
-    gq = _weight(q_weight, "q_weight", d, dev)
-    gk = None if K is None else _weight(k_weight, "k_weight", d, dev)
-    if T == 0:
-        return Qo, Ko
-    _launch(dev, "dsa_norm_rope", q, qs, k, ks, gq, gk, eps, freq, rotary, interleaved, pos, cu, lens, B, T, Hq, Hk, d, qo,
-            qos, ko, kos)
-    return Qo, Ko
+    return _native().norm_rope(Q, K, q_weight, k_weight, inv_freq, positions, cu_seqlens_q, seqlens_k, interleaved, eps, out)
 
 
 def norm_rope_bwd_workspace_bytes(total_q: int, Hq: int, Hk: int, d: int) -> int:
@@ -505,43 +415,8 @@ def norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight=None, k_weight=None, inv_freq=N
     """Gradients (dQ, dK, dq_weight, dk_weight) of norm_rope from those at its outputs: dQ, dK
     bf16, the weights' fp32 [d] (None where there is no weight).  `out` may give (dQ, dK) to
     write, dQ_out and dK_out themselves among them (see dsa_norm_rope_bwd)."""
-    T, Hq, d = Q.shape
-    dev = Q.get_device()
-    q, qs = _rows(Q, "Q", T, Hq, d, dev)
-    dqo, dqos = _rows(dQ_out, "dQ_out", T, Hq, d, dev)
-    Hk, k, ks, dko, dkos = 0, None, 0, None, 0
-    if K is not None:
-        Hk = K.shape[1]
-        k, ks = _rows(K, "K", T, Hk, d, dev)
-        dko, dkos = _rows(dK_out, "dK_out", T, Hk, d, dev)
-    if out is not None:
-        dQ, dK = out
-    else:
-        dQ = torch.empty_like(Q)
-        dK = None if K is None else torch.empty_like(K)
-    dq, dqs = _rows(dQ, "dQ", T, Hq, d, dev)
-    dk, dks = (None, 0) if K is None else _rows(dK, "dK", T, Hk, d, dev)
-    pos, cu, lens, B = _token_map(T, positions, cu_seqlens_q, seqlens_k, dev)
-    freq, rotary = _rope(inv_freq, "inv_freq", dev)
-    gq = _weight(q_weight, "q_weight", d, dev)
-    gk = None if K is None else _weight(k_weight, "k_weight", d, dev)
-    dgq = None if gq is None else torch.empty(d, dtype=torch.float32, device=Q.device)
-    dgk = None if gk is None else torch.empty(d, dtype=torch.float32, device=Q.device)
-    if T == 0:
-        return dQ, dK, None if dgq is None else dgq.zero_(), None if dgk is None else dgk.zero_()
-    if gq is not None or gk is not None:
-        workspace = _workspace(workspace, norm_rope_bwd_workspace_bytes(T, Hq, Hk, d), Q.device, dev)
-    _launch(dev, "dsa_norm_rope_bwd", q, qs, k, ks, dqo, dqos, dko, dkos, gq, gk, eps, freq, rotary, interleaved, pos, cu,
-            lens, B, T, Hq, Hk, d, dq, dqs, dk, dks, _ptr(dgq), _ptr(dgk), _ptr(workspace),
-            0 if workspace is None else workspace.numel())
-    return dQ, dK, dgq, dgk
-
-
-def _table(block_table, seqlens_k, dev: int):
-    """(block_table, max_pages, seqlens_k, batch) as the library takes them."""
-    B, width = block_table.shape
-    return (_arg(block_table, "block_table", _I32, (B, width), dev), width,
-            _arg(seqlens_k, "seqlens_k", _I32, (B,), dev), B)
+    return _native().norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight, k_weight, inv_freq, positions, cu_seqlens_q, seqlens_k,
+                                   interleaved, eps, out, workspace)
 
 
 def cache_append(K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, cu_seqlens_q, seqlens_k, k_weight=None,
@@ -553,118 +428,33 @@ def cache_append(K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, cu_seq
     k_cache, v_cache bf16 [pages, page_size, Hkv, d], k_idx_cache [pages, page_size, d_I];
     block_table int32 [B, max_pages]; seqlens_k int32 [B]: lengths with the new tokens, whose
     last one sits at seqlens_k - 1.  Tokens without a page are dropped (see dsa_cache_append)."""
-    T, Hkv, d = K.shape
-    dev = K.get_device()
-    k, ks = _rows(K, "K", T, Hkv, d, dev)
-    v, vs = _rows(V, "V", T, Hkv, d, dev)
-    table, width, lens, B = _table(block_table, seqlens_k, dev)
-    pages, page = k_cache.shape[:2]
-    kc, kcs = _pool(k_cache, "k_cache", (pages, page, Hkv, d), dev)
-    vc, vcs = _pool(v_cache, "v_cache", (pages, page, Hkv, d), dev)
-    d_I, i, is_, ic, ics = 0, None, 0, None, 0
-    if k_idx is not None:
-        d_I = k_idx.shape[1]
-        i, is_ = _flat_rows(k_idx, "k_idx", T, d_I, dev)
-        ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
-    freq, rotary = _rope(inv_freq, "inv_freq", dev)
-    ifreq, irotary = (None, 0) if k_idx is None else _rope(idx_inv_freq, "idx_inv_freq", dev)
-    pos, cu, _, _ = _token_map(T, positions, cu_seqlens_q, None, dev)
-    if cu_seqlens_q.numel() != B + 1:
-        raise ValueError(f"cu_seqlens_q must have {B + 1} entries, got {cu_seqlens_q.numel()}")
-    gk = _weight(k_weight, "k_weight", d, dev)
-    gi = None if k_idx is None else _weight(k_idx_weight, "k_idx_weight", d_I, dev)
-    if T == 0:
-        return
-    _launch(dev, "dsa_cache_append", k, ks, v, vs, i, is_, gk, gi, eps, freq, rotary, interleaved, ifreq, irotary,
-            idx_interleaved, pos, cu, T, Hkv, d, d_I, kc, kcs, vc, vcs, ic, ics,
-            table, width, lens, B, pages, page)
+    _native().cache_append(K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, cu_seqlens_q, seqlens_k, k_weight,
+                           k_idx_weight, inv_freq, idx_inv_freq, positions, interleaved, idx_interleaved, eps)
 
 
 def index_paged(q_idx, k_idx_cache, w, block_table, seqlens_k, max_seqlen_k: int, scores: Optional[torch.Tensor] = None):
     """Indexer scores of one query row per sequence over the paged indexer keys: fp32 [B, ld].
     Column s < seqlens_k[b] is written; a new `scores` holds -inf elsewhere (see dsa_index_paged)."""
-    B, H_I, d_I = q_idx.shape
-    dev = q_idx.get_device()
-    table, width, lens, _ = _table(block_table, seqlens_k, dev)
-    pages, page = k_idx_cache.shape[:2]
-    ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
-    if scores is None:
-        scores = torch.full((B, _ld(max_seqlen_k)), float("-inf"), dtype=torch.float32, device=q_idx.device)
-    out = _arg(scores, "scores", _F32, (B, scores.shape[1]), dev)
-    _launch(dev, "dsa_index_paged", _arg(q_idx, "q_idx", _BF16, (block_table.shape[0], H_I, d_I), dev), ic, ics,
-            _arg(w, "w", _BF16, (B, H_I), dev), table, width, lens, B, pages, page, max_seqlen_k, H_I, d_I, out,
-            scores.shape[1])
-    return scores
+    return _native().index_paged(q_idx, k_idx_cache, w, block_table, seqlens_k, max_seqlen_k, scores)
 
 
 def sparse_attn_decode_paged(Q, k_cache, v_cache, indices, block_table, seqlens_k, scale: Optional[float] = None, out=None):
     """Attention of one query row per sequence over its selected positions in the paged cache.
     Returns (O [B, Hq, d] bf16, lse [B, Hq] fp32); `out` may give (O, lse) to write, lse None
     for none (see dsa_sparse_attn_decode_paged)."""
-    B, Hq, d = Q.shape
-    dev = Q.get_device()
-    table, width, lens, _ = _table(block_table, seqlens_k, dev)
-    pages, page, Hkv = k_cache.shape[:3]
-    kc, kcs = _pool(k_cache, "k_cache", (pages, page, Hkv, d), dev)
-    vc, vcs = _pool(v_cache, "v_cache", (pages, page, Hkv, d), dev)
-    if out is not None:
-        O, lse = out
-        _arg(O, "O", _BF16, (B, Hq, d), dev)
-        if lse is not None:
-            _arg(lse, "lse", _F32, (B, Hq), dev)
-    else:
-        O = torch.empty_like(Q)
-        lse = torch.empty((B, Hq), dtype=_F32, device=Q.device)
-    _launch(dev, "dsa_sparse_attn_decode_paged", _arg(Q, "Q", _BF16, (block_table.shape[0], Hq, d), dev), kc, kcs,
-            vc, vcs, _arg(indices, "indices", _I32, (B, indices.shape[1]), dev), table, width, lens, B, pages, page, Hq, Hkv, d,
-            indices.shape[1], 1.0 / math.sqrt(d) if scale is None else scale, O.data_ptr(), _ptr(lse))
-    return O, lse
+    return _native().sparse_attn_decode_paged(Q, k_cache, v_cache, indices, block_table, seqlens_k, scale, out)
 
 
 def decode_paged_workspace_bytes(batch: int, max_seqlen_k: int) -> int:
     return _lib.load().dsa_decode_paged_workspace_size(batch, max_seqlen_k)
 
 
-def _decode_out(out, B: int, k: int, Hq: int, d: int, device, dev: int):
-    if out is None:
-        return (torch.empty((B, k), dtype=_I32, device=device),
-                torch.empty((B, Hq, d), dtype=torch.bfloat16, device=device),
-                torch.empty((B, Hq), dtype=torch.float32, device=device))
-    indices, O, lse = out
-    _arg(indices, "indices", _I32, (B, k), dev)
-    _arg(O, "O", _BF16, (B, Hq, d), dev)
-    if lse is not None:
-        _arg(lse, "lse", _F32, (B, Hq), dev)
-    return out
-
-
-def _workspace(workspace, nbytes: int, device, dev: int):
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _arg(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    return workspace
-
-
 def decode_paged(q_idx, w, Q, k_cache, v_cache, k_idx_cache, block_table, seqlens_k, max_seqlen_k: int, k: int,
                  scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None, out=None):
     """Whole DSA decode step of one query row per sequence over a paged cache that holds the
     current token already.  Returns (indices [B, k] int32, O [B, Hq, d] bf16, lse [B, Hq] fp32)."""
-    B, Hq, d = Q.shape
-    H_I, d_I = q_idx.shape[1:]
-    dev = Q.get_device()
-    table, width, lens, _ = _table(block_table, seqlens_k, dev)
-    pages, page, Hkv = k_cache.shape[:3]
-    kc, kcs = _pool(k_cache, "k_cache", (pages, page, Hkv, d), dev)
-    vc, vcs = _pool(v_cache, "v_cache", (pages, page, Hkv, d), dev)
-    ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
-    ws = _workspace(workspace, decode_paged_workspace_bytes(B, max_seqlen_k), Q.device, dev)
-    indices, O, lse = out = _decode_out(out, B, k, Hq, d, Q.device, dev)
-    _launch(dev, "dsa_decode_paged", _arg(q_idx, "q_idx", _BF16, (B, H_I, d_I), dev),
-            _arg(w, "w", _BF16, (B, H_I), dev), _arg(Q, "Q", _BF16, (block_table.shape[0], Hq, d), dev),
-            kc, kcs, vc, vcs, ic, ics, table, width, lens, B, pages, page, max_seqlen_k, Hq, Hkv, d, H_I, d_I, k,
-            1.0 / math.sqrt(d) if scale is None else scale, indices.data_ptr(), O.data_ptr(), _ptr(lse), ws.data_ptr(),
-            ws.numel())
-    return out
+    return _native().decode_paged(q_idx, w, Q, k_cache, v_cache, k_idx_cache, block_table, seqlens_k, max_seqlen_k, k, scale,
+                                  workspace, out)
 
 
 def decode_step_paged_workspace_bytes(batch: int, max_seqlen_k: int, Hq: int, d: int, H_I: int, d_I: int) -> int:
@@ -680,31 +470,9 @@ def decode_step_paged(q_idx, w, Q, K, V, k_idx, k_cache, v_cache, k_idx_cache, b
     (as norm_rope and cache_append do, in one launch), then decode_paged.
 
     Returns (indices [B, k] int32, O [B, Hq, d] bf16, lse [B, Hq] fp32)."""
-    B, Hq, d = Q.shape
-    H_I, d_I = q_idx.shape[1:]
-    dev = Q.get_device()
-    table, width, lens, _ = _table(block_table, seqlens_k, dev)
-    pages, page, Hkv = k_cache.shape[:3]
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
-    kc, kcs = _pool(k_cache, "k_cache", (pages, page, Hkv, d), dev)
-    vc, vcs = _pool(v_cache, "v_cache", (pages, page, Hkv, d), dev)
-    ic, ics = _pool(k_idx_cache, "k_idx_cache", (pages, page, d_I), dev)
-    freq, rotary = _rope(inv_freq, "inv_freq", dev)
-    ifreq, irotary = _rope(idx_inv_freq, "idx_inv_freq", dev)
-    ws = _workspace(workspace, decode_step_paged_workspace_bytes(B, max_seqlen_k, Hq, d, H_I, d_I), Q.device, dev)
-    indices, O, lse = out = _decode_out(out, B, k, Hq, d, Q.device, dev)
-    _launch(dev, "dsa_decode_step_paged", *_rows(q_idx, "q_idx", B, H_I, d_I, dev),
-            _arg(w, "w", _BF16, (B, H_I), dev), *_rows(Q, "Q", B, Hq, d, dev), *_rows(K, "K", B, Hkv, d, dev),
-            *_rows(V, "V", B, Hkv, d, dev), *_flat_rows(k_idx, "k_idx", B, d_I, dev),
-            _weight(q_weight, "q_weight", d, dev), _weight(k_weight, "k_weight", d, dev),
-            _weight(q_idx_weight, "q_idx_weight", d_I, dev), _weight(k_idx_weight, "k_idx_weight", d_I, dev), eps, freq,
-            rotary, interleaved, ifreq, irotary, idx_interleaved,
-            None if positions is None else _arg(positions, "positions", _I32, (B,), dev), kc, kcs, vc, vcs, ic, ics,
-            table, width, lens, B, pages, page, max_seqlen_k, Hq, Hkv, d, H_I, d_I, k,
-            1.0 / math.sqrt(d) if scale is None else scale, indices.data_ptr(), O.data_ptr(), _ptr(lse), ws.data_ptr(),
-            ws.numel())
-    return out
+    return _native().decode_step_paged(q_idx, w, Q, K, V, k_idx, k_cache, v_cache, k_idx_cache, block_table, seqlens_k,
+                                       max_seqlen_k, k, q_weight, k_weight, q_idx_weight, k_idx_weight, inv_freq, idx_inv_freq,
+                                       positions, interleaved, idx_interleaved, eps, scale, workspace, out)
 
 
 def device_status():

@@ -1,11 +1,15 @@
-"""Builds libdsa_b200.so in-tree for sm_100a with nvcc (no JIT, no torch extension)."""
+"""Builds libdsa_b200.so in-tree for sm_100a with nvcc, and with the host compiler the Python
+binding _binding.so of the paged calls over it (no JIT)."""
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdsa_b200.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -35,6 +39,32 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
+def needs_binding() -> bool:
+    hdr = os.path.join(os.path.dirname(HERE), "include", "dsa.h")
+    return not os.path.exists(BINDING) or any(os.path.getmtime(f) > os.path.getmtime(BINDING) for f in (BINDING_SRC, hdr))
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The native marshalling of the paged calls: a Python module on torch's headers that calls the
+    C ABI of libdsa_b200.so beside it."""
+    if not force and not needs_binding():
+        return BINDING
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(tdir, "include"),
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), BINDING_SRC, "-o", BINDING + ".tmp",
+           "-L" + os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-L" + HERE,
+           "-l:libdsa_b200.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
+    build_binding(force="--force" in sys.argv, verbose=True)
