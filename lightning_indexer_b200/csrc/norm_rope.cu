@@ -726,7 +726,7 @@ static int head_rows_bwd_kernel_launch(const dsa::HeadRowsParams& p, int blocks,
     if (const cudaError_t e_ = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e_ != cudaSuccess) return cuda_fail(e_);
     attr_done = true;
   }
-  return launch_pdl(false, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), smem, stream, p);
+  return launch_pdl(true, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), smem, stream, p);
 }
 
 int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], cudaStream_t stream) {

@@ -260,7 +260,7 @@ static int decode_paged_run(const void* q_idx, const void* w, const void* Q, con
                    L.topk_bytes, stream);
   if (st != DSA_OK) return st;
   return sparse_attn_paged_call(Q, k_cache, k_page_stride, v_cache, v_page_stride, indices, table, max_pages, lens,
-                                batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, false, stream);
+                                batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, true, stream);
 }
 
 }  // namespace dsa_host
@@ -285,7 +285,7 @@ DSA_API int dsa_norm_rope(const void* Q, int64_t q_stride, const void* K, int64_
   p.tk = token_map(positions, cu_seqlens_q, seqlens_k, batch, total_q);
   p.seg[p.nseg++] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, Q_out, q_out_stride);
   if (K) p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, K_out, k_out_stride);
-  return head_rows_fwd_launch(p, false, static_cast<cudaStream_t>(stream));
+  return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API size_t dsa_norm_rope_bwd_workspace_size(int64_t total_q, int Hq, int Hk, int d) {
@@ -360,7 +360,7 @@ DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int
   paged_segs(p, K, k_stride, V, v_stride, k_idx, k_idx_stride, k_weight, k_idx_weight, inv_freq, rotary_dim, interleaved,
              idx_inv_freq, idx_rotary_dim, idx_interleaved, Hkv, d, d_I, k_cache, k_page_stride, v_cache, v_page_stride,
              k_idx_cache, k_idx_page_stride, block_table, max_pages, num_pages, page_size);
-  return head_rows_fwd_launch(p, false, static_cast<cudaStream_t>(stream));
+  return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t k_idx_page_stride, const void* w,
@@ -368,7 +368,7 @@ DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t 
                             int num_pages, int page_size, int max_seqlen_k, int H_I, int d_I, float* scores,
                             int64_t ld_scores, void* stream) {
   return index_paged_call(q_idx, k_idx_cache, k_idx_page_stride, w, block_table, max_pages, seqlens_k, batch, num_pages,
-                          page_size, max_seqlen_k, H_I, d_I, scores, ld_scores, nullptr, nullptr, false,
+                          page_size, max_seqlen_k, H_I, d_I, scores, ld_scores, nullptr, nullptr, true,
                           static_cast<cudaStream_t>(stream));
 }
 
@@ -378,7 +378,7 @@ DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int
                                          int batch, int num_pages, int page_size, int Hq, int Hkv, int d, int k,
                                          float scale, void* O, float* lse, void* stream) {
   return sparse_attn_paged_call(Q, k_cache, k_page_stride, v_cache, v_page_stride, indices, block_table, max_pages,
-                                seqlens_k, batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, false,
+                                seqlens_k, batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, true,
                                 static_cast<cudaStream_t>(stream));
 }
 
@@ -403,7 +403,7 @@ DSA_API int dsa_decode_paged(const void* q_idx, const void* w, const void* Q, co
     return DSA_ERR_WORKSPACE;
   return decode_paged_run(q_idx, w, Q, k_cache, k_page_stride, v_cache, v_page_stride, k_idx_cache, k_idx_page_stride,
                           block_table, max_pages, seqlens_k, batch, num_pages, page_size, max_seqlen_k, Hq, Hkv, d, H_I,
-                          d_I, k, scale, indices, O, lse, workspace, false, static_cast<cudaStream_t>(stream));
+                          d_I, k, scale, indices, O, lse, workspace, true, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API size_t dsa_decode_step_paged_workspace_size(int batch, int max_seqlen_k, int Hq, int d, int H_I, int d_I) {
@@ -457,7 +457,7 @@ DSA_API int dsa_decode_step_paged(const void* q_idx, int64_t q_idx_stride, const
              idx_inv_freq, idx_rotary_dim, idx_interleaved, Hkv, d, d_I, k_cache, k_page_stride, v_cache, v_page_stride,
              k_idx_cache, k_idx_page_stride, block_table, max_pages, num_pages, page_size);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (st = head_rows_fwd_launch(p, false, s); st != DSA_OK) return st;
+  if (st = head_rows_fwd_launch(p, true, s); st != DSA_OK) return st;
   return decode_paged_run(qi_out, w, q_out, k_cache, k_page_stride, v_cache, v_page_stride, k_idx_cache,
                           k_idx_page_stride, block_table, max_pages, seqlens_k, batch, num_pages, page_size,
                           max_seqlen_k, Hq, Hkv, d, H_I, d_I, k, scale, indices, O, lse, ws, true, s);
