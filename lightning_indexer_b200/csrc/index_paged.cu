@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(192, 1)
         const int s = t * 128 + lane_grp * 32 + lane;
         const bool in_pool = s < w.len && (unsigned)__ldg(row + (s >> p.page_shift)) < (unsigned)p.num_pages;
         if (!(ok = mbar_wait(&acc_full[ab], abph, abort_flag, 46))) break;
+        __syncwarp();  // the loads below are warp-wide
         tc_fence_after();
         const uint32_t tbase = tmem_base + lane_off + ab * C::N;
         float acc = 0.f;
