@@ -39,8 +39,8 @@ struct HeadSeg {
   int interleaved, paged;
   int block0;           // first block of this tensor's rows
   int groups;           // warp-sized groups of 512 / D rows
-  int iters;            // groups of a run (forward: of a warp), at most 32 tokens' worth
-  int warp_iters;       // backward: groups of a warp
+  int iters;            // groups of a run, at most 32 tokens' worth
+  int warps;            // warps of this tensor (whole blocks)
   unsigned div_mul;     // row / heads = (row * div_mul) >> div_shift for rows < 2^31
   int div_shift;
   float* dg_part;       // backward with norm: [blocks of this tensor][D]
@@ -327,27 +327,58 @@ __device__ __forceinline__ int rows_mode(const HeadSeg& s) {
 constexpr int NR_STAGES = 4;  // groups in flight per warp
 constexpr int NR_GROUP_BYTES = 1024;
 
+// A warp's groups: runs of s.iters consecutive ones, the runs w, w + warps, w + 2 warps, ... of
+// the tensor, so that all warps move through memory side by side.
+struct WarpRuns {
+  int n;          // groups of this warp
+  unsigned row0;  // its first row
+  __device__ __forceinline__ WarpRuns(const HeadSeg& s, int w, int rpw) {
+    const int nruns = (s.groups + s.iters - 1) / s.iters;
+    const int mine = w < nruns ? (nruns - 1 - w) / s.warps + 1 : 0;
+    n = mine * s.iters;
+    if (mine > 0 && w + (mine - 1) * s.warps == nruns - 1) n -= nruns * s.iters - s.groups;
+    row0 = (unsigned)w * (unsigned)(s.iters * rpw);
+  }
+};
+
 // A lane's row as the warp steps through its groups.  SHARED: the heads fill whole groups, so
-// all rows of a group belong to one token and the token is found by counting.
-template <bool SHARED, int RPW>
+// all rows of a group belong to one token and, inside a run, the token is found by counting.
+// RUNS: the warp goes on to further runs.
+template <bool SHARED, bool RUNS, int RPW>
 struct RowCursor {
   unsigned r, h;
-  int t;
-  __device__ __forceinline__ RowCursor(const HeadSeg& s, unsigned row) : r(row) {
+  int t, left;  // left: groups of the run from this one on
+  __device__ __forceinline__ RowCursor(const HeadSeg& s, unsigned row) : r(row), left(s.iters) { find(s); }
+  __device__ __forceinline__ void find(const HeadSeg& s) {
     t = row_token(s, r);
     h = r - (unsigned)t * (unsigned)s.heads;
   }
   __device__ __forceinline__ void step(const HeadSeg& s) {
+    if (RUNS && --left == 0) {
+      left = s.iters;
+      r += RPW + (unsigned)(s.warps - 1) * (unsigned)(s.iters * RPW);
+      find(s);
+      return;
+    }
     r += RPW;
     if (SHARED) {
       h += RPW;
       if (h >= (unsigned)s.heads) h -= (unsigned)s.heads, ++t;
     } else {
-      t = row_token(s, r);
-      h = r - (unsigned)t * (unsigned)s.heads;
+      find(s);
     }
   }
 };
+
+// Looks up the tokens of the run that starts at `row` (`left` groups of the warp from there on);
+// returns the first token.
+__device__ __forceinline__ int runs_look_up(const TokenMap& tk, const HeadSeg& s, RunPlaces& all, unsigned row, int left,
+                                            int rpw, unsigned rows, int lane) {
+  const int t_first = row_token(s, row);
+  all.look_up(tk, s, t_first, left > 0 ? row_token(s, min(row + (unsigned)(min(s.iters, left) * rpw), rows) - 1) : t_first - 1,
+              lane);
+  return t_first;
+}
 
 template <int D, bool INTER, int MODE>
 __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane,
@@ -359,11 +390,11 @@ __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const Hea
   const L col(s, sub);
   const bool norm = FULL || s.g != nullptr, turned = FULL || s.inv_freq != nullptr;
   const unsigned rows = (unsigned)p.tk.T * (unsigned)s.heads;
-  const int grp0 = warp_in_seg * s.iters, n = min(s.iters, s.groups - grp0);
+  const int grp0 = warp_in_seg * s.iters, n = min(s.iters, s.groups - grp0);  // one run
   const unsigned row0 = (unsigned)grp0 * L::RPW, row_end = n > 0 ? min(row0 + n * L::RPW, rows) : row0;
   const uint32_t mine = smem_u32(ring) + lane * 16;
   const int de = col.e1 - col.e0;
-  RowCursor<SHARED, L::RPW> ahead(s, row0 + rg), at = ahead;
+  RowCursor<SHARED, false, L::RPW> ahead(s, row0 + rg), at = ahead;
   uint32_t fill = 0, use = 0;
   auto issue = [&] {
     if (ahead.r < row_end) {
@@ -378,8 +409,9 @@ __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const Hea
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue();
   const int t_first = row_token(s, row0), t_last = n > 0 ? row_token(s, row_end - 1) : t_first - 1;
-  RunPlaces all, cur;
+  RunPlaces all, cur;  // looked up while the first rows fly
   all.look_up(p.tk, s, t_first, t_last, lane);
+  int cur_t = -1;
   uint4 ga = {}, gb = {};
   if (norm) {
     ga = *reinterpret_cast<const uint4*>(s.g + col.e0);
@@ -390,7 +422,6 @@ __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const Hea
   unpack8(gb, g1);
   load_steps(s, ts);
   LaneTurns turns;
-  int cur_t = -1;
 #pragma unroll 1
   for (int it = 0; it < n; ++it) {
     issue();
@@ -473,15 +504,15 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
   const L col(s, sub);
   const bool norm = FULL || s.g != nullptr, turned = FULL || s.inv_freq != nullptr;
   const unsigned rows = (unsigned)p.tk.T * (unsigned)s.heads;
-  const int grp0 = (int)min((long long)warp_in_seg * s.warp_iters, (long long)s.groups);
-  const int n = min(s.warp_iters, s.groups - grp0);
-  const unsigned row0 = (unsigned)grp0 * L::RPW, row_end = min(row0 + n * L::RPW, rows);
+  const WarpRuns runs(s, warp_in_seg, L::RPW);
+  const int n = runs.n;
   const uint32_t mine = smem_u32(ring) + lane * 16;
   const int de = col.e1 - col.e0;
-  RowCursor<SHARED, L::RPW> ahead(s, row0 + rg), at = ahead;
+  RowCursor<SHARED, true, L::RPW> ahead(s, runs.row0 + rg), at = ahead;
+  int issued = 0;
   uint32_t fill = 0, use = 0;
   auto issue = [&] {
-    if (ahead.r < row_end) {
+    if (issued < n && (SHARED || ahead.r < rows)) {
       const int in_token = (int)(ahead.h * D + col.e0);
       const uint16_t* src = s.dy + (long long)ahead.t * s.dy_stride + in_token;
       cp_async_16(mine + fill, src, true);
@@ -494,6 +525,7 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
     }
     cp_async_commit();
     ahead.step(s);
+    ++issued;
     fill = (fill + 2 * NR_GROUP_BYTES) & (2 * S * NR_GROUP_BYTES - 1);
   };
 #pragma unroll
@@ -509,16 +541,13 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
   for (int i = 0; i < 4; ++i) dg0[i] = dg1[i] = f2(0.f, 0.f);
   LaneTurns turns;
   RunPlaces all, cur;
-  int cur_t = -1, t_first = 0, run_end = 0;
+  int cur_t = -1, t_first = 0;
 #pragma unroll 1
   for (int it = 0; it < n; ++it) {
-    if (it == run_end) {  // the next run's tokens
-      run_end = min(it + s.iters, n);
-      t_first = row_token(s, row0 + it * L::RPW);
-      all.look_up(p.tk, s, t_first, row_token(s, min(row0 + run_end * L::RPW, rows) - 1), lane);
-    }
+    if (at.left == s.iters)  // a new run's tokens
+      t_first = runs_look_up(p.tk, s, all, at.r - rg, n - it, L::RPW, rows, lane), cur_t = -1;
     issue();
-    const bool in = SHARED || at.r < row_end;
+    const bool in = SHARED || at.r < rows;
     const int t = in ? at.t : t_first;
     if (SHARED ? t != cur_t : __any_sync(0xffffffffu, t != cur_t)) {
       cur_t = t;
@@ -658,10 +687,16 @@ static long long seg_groups(const dsa::HeadRowsParams& p, const dsa::HeadSeg& s)
   const long long rpw = 512 / s.D;
   return ((long long)p.tk.T * s.heads + rpw - 1) / rpw;
 }
-// Fills in what the kernels read of each segment; a warp takes s.warp_iters groups where that
-// is set, else one run.  Returns the number of blocks.
-static int plan_segs(dsa::HeadRowsParams& p, int run) {
-  long long block = 0;
+// What a group of a tensor costs, in tenths of one whose turns are at hand: a token's turns
+// cost about 4 and are paid once per token and run.
+static int group_weight(const dsa::HeadSeg& s) { return 10 + 4 * (512 / s.D) / std::max(s.heads, 512 / s.D); }
+
+// Fills in what the kernels read of each segment: runs of up to `run` groups, dealt to about
+// `warps` warps in all, to the tensors by their cost (0: a warp for each run).  Returns the
+// number of blocks.
+static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps) {
+  long long cost = 1, block = 0;
+  for (int i = 0; i < p.nseg; ++i) cost += seg_groups(p, p.seg[i]) * group_weight(p.seg[i]);
   for (int i = 0; i < p.nseg; ++i) {
     dsa::HeadSeg& s = p.seg[i];
     const int rpw = 512 / s.D;
@@ -673,16 +708,22 @@ static int plan_segs(dsa::HeadRowsParams& p, int run) {
     s.div_shift = 31 + lg;
     s.div_mul = (unsigned)(((1ULL << (31 + lg)) + s.heads - 1) / s.heads);
     s.block0 = (int)block;
-    const long long per_block = (long long)(s.warp_iters ? s.warp_iters : s.iters) * dsa::NR_WARPS;
-    block += (s.groups + per_block - 1) / per_block;
+    const long long nruns = ((long long)s.groups + s.iters - 1) / s.iters;
+    const long long share = warps ? (warps * s.groups * group_weight(s) + cost - 1) / cost : nruns;
+    const long long blocks = (std::min(nruns, std::max<long long>(share, 1)) + dsa::NR_WARPS - 1) / dsa::NR_WARPS;
+    s.warps = (int)(blocks * dsa::NR_WARPS);
+    block += blocks;
   }
   return (int)block;
 }
 
+// Forward: a warp for every run.  Blocks that come and go balance rows of different cost: at
+// 32768 tokens of 32 + 4 heads 102 us, against 106 to 142 us in one wave of warps that walk
+// many runs, by how the tensors' costs are weighted; an append of as many, 34 against 48 to 58.
 int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) {
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
-  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1);
+  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1, 0);
   int d = p.seg[0].D, inter = p.seg[0].interleaved;
   for (int i = 1; i < p.nseg; ++i) {
     if (p.seg[i].D != d || p.seg[i].interleaved != inter) d = 0;
@@ -697,25 +738,24 @@ int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) 
   return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), 0, stream, p);
 }
 
-// Groups per warp of the backward, so that the whole call is at most 16 warps' worth per SM.
-// A token's turns cost about 0.4 of a group and are paid once per token and warp: tensors with
-// few heads get fewer groups per warp.
-static int bwd_weight(int heads, int d) { return 10 + 4 * (512 / d) / std::max(heads, 512 / d); }
-static int bwd_iters(long long T, int Hq, int Hk, int d, int heads) {
-  const long long rpw = 512 / d, nq = (T * Hq + rpw - 1) / rpw, nk = (T * Hk + rpw - 1) / rpw;
-  const long long warps = 15LL * sm_count();  // the last block of each tensor may be part empty
-  const long long budget = (nq * bwd_weight(Hq, d) + (Hk ? nk * bwd_weight(Hk, d) : 0) + warps - 1) / warps;
-  return (int)std::max<long long>(1, (budget + bwd_weight(heads, d) - 1) / bwd_weight(heads, d));
+// Blocks of the backward: one wave, at most 16 warps per SM, since each block adds a share to
+// the weights' gradients.  They set the order of those sums and the size of the workspace, so
+// they follow from the sizes alone.
+static int bwd_plan(dsa::HeadRowsParams& p) {
+  const long long warps = 15LL * sm_count();  // the last block of a tensor may be part empty
+  long long groups = 0;
+  for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
+  return plan_segs(p, (int)std::max<long long>(1, std::min<long long>(8, groups / warps)), warps);
 }
 size_t norm_rope_bwd_ws_bytes(long long T, int Hq, int Hk, int d) {
-  const long long rpw = 512 / d;
-  long long blocks = 0;
+  dsa::HeadRowsParams p{};
+  p.tk.T = (int)std::min<long long>(T, INT_MAX);
   for (int H : {Hq, Hk}) {
     if (H == 0) continue;
-    const long long per_block = (long long)bwd_iters(T, Hq, Hk, d, H) * dsa::NR_WARPS;
-    blocks += ((T * H + rpw - 1) / rpw + per_block - 1) / per_block;
+    p.seg[p.nseg].heads = H;
+    p.seg[p.nseg++].D = d;
   }
-  return (size_t)blocks * d * sizeof(float);
+  return (size_t)bwd_plan(p) * d * sizeof(float);
 }
 template <int D, int INTER>
 static int head_rows_bwd_kernel_launch(const dsa::HeadRowsParams& p, int blocks, cudaStream_t stream) {
@@ -730,10 +770,7 @@ static int head_rows_bwd_kernel_launch(const dsa::HeadRowsParams& p, int blocks,
 }
 
 int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], cudaStream_t stream) {
-  const int Hk = p.nseg > 1 ? p.seg[1].heads : 0;
-  for (int i = 0; i < p.nseg; ++i)
-    p.seg[i].warp_iters = bwd_iters(p.tk.T, p.seg[0].heads, Hk, p.seg[i].D, p.seg[i].heads);
-  const int blocks = plan_segs(p, 8);
+  const int blocks = bwd_plan(p);
   dsa::DgParams q{};
   int n = 0;
   for (int i = 0; i < p.nseg; ++i) {
