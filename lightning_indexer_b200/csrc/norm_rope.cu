@@ -60,7 +60,8 @@ struct TokenMap {
 };
 
 constexpr int NR_MAX_SEGS = 5;
-constexpr int NR_WARPS = 8;
+constexpr int NR_FWD_WARPS = 4;  // warps of a block; 5 blocks per SM at 102 registers (8 x 3 spills, 8 x 2 waits)
+constexpr int NR_BWD_WARPS = 8;  // 2 blocks per SM
 
 struct HeadRowsParams {
   HeadSeg seg[NR_MAX_SEGS];
@@ -218,8 +219,9 @@ struct LaneCols {
 // The turn steps of the block's segment and, per warp, the (cos, sin) of one token's pairs.
 struct TurnSmem {
   unsigned long long step[64];
-  __align__(16) float2 cs[NR_WARPS][64];
+  __align__(16) float2 cs[NR_BWD_WARPS][64];
 };
+static_assert(NR_FWD_WARPS <= NR_BWD_WARPS, "one exchange buffer per warp");
 __device__ __forceinline__ void load_steps(const HeadSeg& s, TurnSmem& ts) {
   if (!s.inv_freq) return;  // block-uniform
   if (threadIdx.x < s.rotary / 2) ts.step[threadIdx.x] = turn_step(s.inv_freq[threadIdx.x]);
@@ -475,13 +477,13 @@ __device__ __forceinline__ int block_seg(const HeadRowsParams& p) {
 // D and INTER (0 or 1) of every segment where they agree, else 0 and -1: the call is then
 // dispatched per segment, at the registers of the largest form.
 template <int D, int INTER>
-__global__ void __launch_bounds__(NR_WARPS * 32, 3) head_rows_fwd_kernel(const __grid_constant__ HeadRowsParams p) {
+__global__ void __launch_bounds__(NR_FWD_WARPS * 32, 5) head_rows_fwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ __align__(16) uint8_t rings[NR_WARPS][NR_STAGES * NR_GROUP_BYTES];
+  __shared__ __align__(16) uint8_t rings[NR_FWD_WARPS][NR_STAGES * NR_GROUP_BYTES];
   __shared__ TurnSmem ts;
   const HeadSeg& s = p.seg[block_seg(p)];
-  const int w = ((int)blockIdx.x - s.block0) * NR_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int w = ((int)blockIdx.x - s.block0) * NR_FWD_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
   uint8_t* ring = rings[threadIdx.x / 32];
   const int mode = rows_mode(s);
 #define DSA_HEAD_ROWS(DD, II)                                                            \
@@ -624,28 +626,28 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < D; i += NR_WARPS * 32) {
+  for (int i = threadIdx.x; i < D; i += NR_BWD_WARPS * 32) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < NR_WARPS; ++w) v += acc_smem[w * D + i];
+    for (int w = 0; w < NR_BWD_WARPS; ++w) v += acc_smem[w * D + i];
     s.dg_part[(long long)((int)blockIdx.x - s.block0) * D + i] = v;
   }
 }
 
 struct HeadRowsBwdSmem {
-  __align__(16) uint8_t rings[NR_WARPS][NR_STAGES * 2 * NR_GROUP_BYTES];
+  __align__(16) uint8_t rings[NR_BWD_WARPS][NR_STAGES * 2 * NR_GROUP_BYTES];
   TurnSmem ts;
-  float acc[NR_WARPS * 128];
+  float acc[NR_BWD_WARPS * 128];
 };
 
 template <int D, int INTER>
-__global__ void __launch_bounds__(NR_WARPS * 32, 2) head_rows_bwd_kernel(const __grid_constant__ HeadRowsParams p) {
+__global__ void __launch_bounds__(NR_BWD_WARPS * 32, 2) head_rows_bwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   HeadRowsBwdSmem& sm = *reinterpret_cast<HeadRowsBwdSmem*>(smem_raw);
   const HeadSeg& s = p.seg[block_seg(p)];
-  const int w = ((int)blockIdx.x - s.block0) * NR_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int w = ((int)blockIdx.x - s.block0) * NR_BWD_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
   uint8_t* ring = sm.rings[threadIdx.x / 32];
   const int mode = rows_mode(s);
   if (mode == ROWS_FULL) head_rows_bwd<D, INTER, ROWS_FULL>(p, s, w, lane, ring, sm.ts, sm.acc);
@@ -694,7 +696,7 @@ static int group_weight(const dsa::HeadSeg& s) { return 10 + 4 * (512 / s.D) / s
 // Fills in what the kernels read of each segment: runs of up to `run` groups, dealt to about
 // `warps` warps in all, to the tensors by their cost (0: a warp for each run).  Returns the
 // number of blocks.
-static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps) {
+static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps, int block_warps) {
   long long cost = 1, block = 0;
   for (int i = 0; i < p.nseg; ++i) cost += seg_groups(p, p.seg[i]) * group_weight(p.seg[i]);
   for (int i = 0; i < p.nseg; ++i) {
@@ -710,8 +712,8 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps) {
     s.block0 = (int)block;
     const long long nruns = ((long long)s.groups + s.iters - 1) / s.iters;
     const long long share = warps ? (warps * s.groups * group_weight(s) + cost - 1) / cost : nruns;
-    const long long blocks = (std::min(nruns, std::max<long long>(share, 1)) + dsa::NR_WARPS - 1) / dsa::NR_WARPS;
-    s.warps = (int)(blocks * dsa::NR_WARPS);
+    const long long blocks = (std::min(nruns, std::max<long long>(share, 1)) + block_warps - 1) / block_warps;
+    s.warps = (int)(blocks * block_warps);
     block += blocks;
   }
   return (int)block;
@@ -723,7 +725,7 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps) {
 int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) {
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
-  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1, 0);
+  const int blocks = plan_segs(p, groups > 32LL * sm_count() ? 8 : 1, 0, dsa::NR_FWD_WARPS);
   int d = p.seg[0].D, inter = p.seg[0].interleaved;
   for (int i = 1; i < p.nseg; ++i) {
     if (p.seg[i].D != d || p.seg[i].interleaved != inter) d = 0;
@@ -735,7 +737,7 @@ int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) 
               : d == 32 && inter ? dsa::head_rows_fwd_kernel<32, 1>
               : d == 32          ? dsa::head_rows_fwd_kernel<32, 0>
                                  : dsa::head_rows_fwd_kernel<0, -1>;
-  return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), 0, stream, p);
+  return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_FWD_WARPS * 32), 0, stream, p);
 }
 
 // Blocks of the backward: one wave, at most 16 warps per SM, since each block adds a share to
@@ -745,7 +747,7 @@ static int bwd_plan(dsa::HeadRowsParams& p) {
   const long long warps = 15LL * sm_count();  // the last block of a tensor may be part empty
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
-  return plan_segs(p, (int)std::max<long long>(1, std::min<long long>(8, groups / warps)), warps);
+  return plan_segs(p, (int)std::max<long long>(1, std::min<long long>(8, groups / warps)), warps, dsa::NR_BWD_WARPS);
 }
 size_t norm_rope_bwd_ws_bytes(long long T, int Hq, int Hk, int d) {
   dsa::HeadRowsParams p{};
@@ -766,7 +768,7 @@ static int head_rows_bwd_kernel_launch(const dsa::HeadRowsParams& p, int blocks,
     if (const cudaError_t e_ = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); e_ != cudaSuccess) return cuda_fail(e_);
     attr_done = true;
   }
-  return launch_pdl(true, kern, dim3((unsigned)blocks), dim3(dsa::NR_WARPS * 32), smem, stream, p);
+  return launch_pdl(true, kern, dim3((unsigned)blocks), dim3(dsa::NR_BWD_WARPS * 32), smem, stream, p);
 }
 
 int head_rows_bwd_launch(dsa::HeadRowsParams& p, float* ws, float* const dg[2], cudaStream_t stream) {
