@@ -41,12 +41,15 @@ struct IndexPagedCfg {
   static constexpr int KSTEPS = PANEL / 16;
   static constexpr int A_BYTES = 128 * D_I * 2;
   static constexpr int B_BYTES = N * D_I * 2;
-  static constexpr int A_STAGES = 6, B_STAGES = 2;
-  static constexpr int TMEM_COLS = 2 * N <= 32 ? 32 : 2 * N <= 64 ? 64 : 128;
-  static constexpr int THREADS = 192;
+  static constexpr int A_STAGES = D_I == 128 ? 6 : D_I == 64 ? 12 : 16;  // 192 KB of keys in flight, or 128
+  static constexpr int B_STAGES = 2, ACCS = 2;                           // accumulators in tensor memory
+  static constexpr int TMEM_COLS = ACCS * N;
+  static constexpr int PRODUCERS = 2;  // warps that load: warp 0 and the last one, every other tile each
+  static constexpr int THREADS = 224;
+  static_assert(A_STAGES % PRODUCERS == 0, "a producer's stages are its own");
   static constexpr int OFF_B = A_STAGES * A_BYTES;
   static constexpr int OFF_BAR = OFF_B + B_STAGES * B_BYTES;
-  static constexpr int NUM_BARS = 2 * A_STAGES + 2 * B_STAGES + 5;
+  static constexpr int NUM_BARS = 2 * A_STAGES + 2 * B_STAGES + 2 * ACCS + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
   static constexpr uint32_t IDESC = idesc_bf16_f32(128, N);
@@ -82,7 +85,7 @@ struct TileWalk {
 };
 
 template <int H_I, int D_I>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(224, 1)
     index_paged_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_q,
                        const IndexPagedParams p) {
   using C = IndexPagedCfg<H_I, D_I>;
@@ -95,18 +98,19 @@ __global__ void __launch_bounds__(192, 1)
   uint64_t* b_full = a_empty + C::A_STAGES;
   uint64_t* b_empty = b_full + C::B_STAGES;
   uint64_t* acc_full = b_empty + C::B_STAGES;
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* mma_done = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + C::ACCS;
+  uint64_t* mma_done = acc_empty + C::ACCS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 16);  // first sequence and tile of this CTA
-  __shared__ long long warp_tiles[6], warp_keys[6];
+  constexpr int WARPS = C::THREADS / 32;
+  __shared__ long long warp_tiles[WARPS], warp_keys[WARPS];
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::A_STAGES; ++i) mbar_init(&a_full[i], 1), mbar_init(&a_empty[i], 1);
     for (int i = 0; i < C::B_STAGES; ++i) mbar_init(&b_full[i], 1), mbar_init(&b_empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
+    for (int i = 0; i < C::ACCS; ++i) mbar_init(&acc_full[i], 1), mbar_init(&acc_empty[i], 4);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(192, 1)
     __syncthreads();
     long long bt = xt - tiles, bk = xk - keys, total = 0;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
       if (i < warp) bt += warp_tiles[i], bk += warp_keys[i];
       total += warp_tiles[i];
     }
@@ -174,8 +178,11 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t tmem_base = *tmem_holder;
   const int b0 = count > 0 ? s_start[0] : 0, t0 = count > 0 ? s_start[1] : 0;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (whole warp)
+  if (warp == 0 || warp == WARPS - 1) {
+    // ------------------------------------------------------------ TMA producers (whole warps)
+    // A page piece costs a warp about 50 ns to issue, 16 pieces to a tile of 16-row pages: two
+    // warps take the tiles by turns.
+    const int producer = warp == 0 ? 0 : 1;
     const int box_rows = min(1 << p.page_shift, 128);
     const int pieces = 128 / box_rows;  // of a tile
     const int piece = lane / C::NPANEL, panel = lane % C::NPANEL;
@@ -185,27 +192,37 @@ __global__ void __launch_bounds__(192, 1)
     bool ok = true;
     for (TileWalk w(p, count, b0, t0); w.left > 0 && ok; w.next()) {
       const int* row = p.table + (long long)w.b * p.table_width;
-      // the page of this lane's piece of tile t (num_pages, past the pool, loads zeros)
-      auto page_of = [&](int t) {
-        const int s = t * 128 + piece * box_rows;
-        if (!mine || s >= w.len) return p.num_pages;
-        const int id = __ldg(row + (s >> p.page_shift));
-        return (unsigned)id < (unsigned)p.num_pages ? id : p.num_pages;
+      // The pages of 32 consecutive pieces of the sequence, one per lane, loaded a batch ahead
+      // and looked at only when used: a lookup per tile put a memory latency into every tile.
+      auto pages_from = [&](int q) {
+        const long long s = (long long)(q + lane) * box_rows;
+        return s < w.len ? __ldg(row + (int)(s >> p.page_shift)) : -1;
       };
-      int page = page_of(w.t);
-      if (lane == 0) {
+      int q0 = w.t * pieces, ids = pages_from(q0), ids_next = pages_from(q0 + 32);
+      if (producer == 0 && lane == 0) {
         if ((ok = mbar_wait(&b_empty[bs], bph ^ 1, abort_flag, 41))) {
           mbar_arrive_expect_tx(&b_full[bs], C::B_BYTES);
           for (int pn = 0; pn < C::NPANEL; ++pn)
             tma_load_2d(sB + bs * C::B_BYTES + pn * C::N * C::SWZ, &tmap_q, &b_full[bs], pn * C::PANEL, w.b * H_I);
         }
       }
+      if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
       if (++bs == C::B_STAGES) { bs = 0; bph ^= 1; }
       const int end = w.t + w.here();
       for (int t = w.t; t < end; ++t) {
-        const int cur = page;
-        if (t + 1 < end) page = page_of(t + 1);
-        if (lane == 0 && ok) {
+        if (t * pieces == q0 + 32) {
+          q0 += 32;
+          ids = ids_next;
+          ids_next = pages_from(q0 + 32);
+        }
+        if (as % C::PRODUCERS != producer) {  // the other warp's stage
+          if (++as == C::A_STAGES) { as = 0; aph ^= 1; }
+          continue;
+        }
+        // a page outside the pool loads zeros: num_pages is past the map's last one
+        const int id = __shfl_sync(0xffffffffu, ids, (t * pieces - q0 + piece) & 31);
+        const int cur = (unsigned)id < (unsigned)p.num_pages ? id : p.num_pages;
+        if (lane == 0) {
           if ((ok = mbar_wait(&a_empty[as], aph ^ 1, abort_flag, 42))) mbar_arrive_expect_tx(&a_full[as], C::A_BYTES);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -219,12 +236,12 @@ __global__ void __launch_bounds__(192, 1)
     }
     if (!ok && lane == 0) {
       // drain: let every load this warp issued land before the CTA can exit
-      for (int i = 0; i < C::A_STAGES; ++i) {
+      for (int i = producer; i < C::A_STAGES; i += C::PRODUCERS) {
         const uint64_t t1 = globaltimer_ns();
         while (!mbar_try_wait(smem_u32(&a_full[i]), aph ^ (i >= as ? 1u : 0u)) && globaltimer_ns() - t1 < 200000000ull) {
         }
       }
-      for (int i = 0; i < C::B_STAGES; ++i) {
+      for (int i = 0; i < C::B_STAGES && producer == 0; ++i) {
         const uint64_t t1 = globaltimer_ns();
         while (!mbar_try_wait(smem_u32(&b_full[i]), bph ^ (i >= bs ? 1u : 0u)) && globaltimer_ns() - t1 < 200000000ull) {
         }
@@ -255,7 +272,7 @@ __global__ void __launch_bounds__(192, 1)
           umma_commit(&a_empty[as]);
           umma_commit(&acc_full[ab]);
           if (++as == C::A_STAGES) { as = 0; aph ^= 1; }
-          if (++ab == 2) { ab = 0; abph ^= 1; }
+          if (++ab == C::ACCS) { ab = 0; abph ^= 1; }
         }
         if (!ok) break;
         umma_commit(&b_empty[bs]);
@@ -287,9 +304,12 @@ __global__ void __launch_bounds__(192, 1)
       const int* row = p.table + (long long)w.b * p.table_width;
       float* out = p.scores + (long long)w.b * p.ld;
       const int end = w.t + w.here();
+      auto page_at = [&](int s) { return s < w.len ? __ldg(row + (s >> p.page_shift)) : -1; };
+      int id_next = page_at(w.t * 128 + lane_grp * 32 + lane);
       for (int t = w.t; t < end; ++t) {
         const int s = t * 128 + lane_grp * 32 + lane;
-        const bool in_pool = s < w.len && (unsigned)__ldg(row + (s >> p.page_shift)) < (unsigned)p.num_pages;
+        const int id = id_next;
+        id_next = page_at(s + 128);  // a tile ahead of its use
         if (!(ok = mbar_wait(&acc_full[ab], abph, abort_flag, 46))) break;
         __syncwarp();  // the loads below are warp-wide
         tc_fence_after();
@@ -306,8 +326,8 @@ __global__ void __launch_bounds__(192, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[ab]);
-        if (s < w.len) out[s] = in_pool ? acc : -INFINITY;
-        if (++ab == 2) { ab = 0; abph ^= 1; }
+        if (s < w.len) out[s] = (unsigned)id < (unsigned)p.num_pages ? acc : -INFINITY;
+        if (++ab == C::ACCS) { ab = 0; abph ^= 1; }
       }
     }
   }
