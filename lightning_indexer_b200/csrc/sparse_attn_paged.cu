@@ -16,11 +16,16 @@
 // in the same order.
 #include <algorithm>
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "warp_mma.cuh"
 
 namespace dsa {
+
+__device__ __forceinline__ void cp_async_16_all(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 struct SAPagedParams {
   const uint16_t* Q;  // [rows, Hq, D]
@@ -41,23 +46,26 @@ constexpr int SAP_MAX_SPLITS = 8;  // blocks of a cluster (the portable limit)
 
 template <int D, int WARPS, int STAGES>
 struct SAPagedSmem {
-  static constexpr int STAGE_BYTES = 2 * 16 * D * 2;  // K and V rows of a chunk
+  static constexpr int ROW = D * 2 + 16;              // padded: ldmatrix meets no bank twice
+  static constexpr int STAGE_BYTES = 2 * 16 * ROW;    // K and V rows of a chunk
+  static constexpr int TILE_BYTES = STAGE_BYTES / 2;
   static constexpr int RING = WARPS * STAGES * STAGE_BYTES;
-  static constexpr int OFF_ML = RING;                    // [WARPS][8] float4: max, sum, rounded sum
+  static constexpr int OFF_ML = RING;                    // [WARPS][8] float2: max, sum
   // what the cluster's blocks send to this one: the states of all of them, and their O of the
-  // outputs that this block finishes (outputs rank, rank + splits, ... of the 8 D)
-  static constexpr int OFF_CML = OFF_ML + WARPS * 8 * 16;             // [splits][8] float4
-  static constexpr int OFF_CO = OFF_CML + SAP_MAX_SPLITS * 8 * 16;    // [splits][ceil(8 D / splits)]
-  static constexpr int BYTES = OFF_CO + (8 * D + SAP_MAX_SPLITS) * 4;
+  // pieces (four dims of a head) that this block finishes
+  static constexpr int OFF_CML = OFF_ML + WARPS * 8 * 8;             // [splits][8] float2
+  static constexpr int OFF_CO = OFF_CML + SAP_MAX_SPLITS * 8 * 8;    // [splits][G D / 4 / splits] float4
+  static constexpr int BYTES = OFF_CO + 8 * D * 4;
+  static_assert(OFF_CO % 16 == 0, "float4");
   static_assert(STAGES * STAGE_BYTES >= 8 * D * 4, "a warp's O replaces its ring");
 };
 
-template <int D, int WARPS, int STAGES>
+// SAME: both caches have the same page stride.
+template <int D, int WARPS, int STAGES, bool SAME>
 __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAPagedParams p, int splits) {
   namespace cg = cooperative_groups;
   using C = SAPagedSmem<D, WARPS, STAGES>;
-  constexpr int SEGS = D / 8, MT = D / 16;
-  constexpr int TILE_BYTES = C::STAGE_BYTES / 2;
+  constexpr int MT = D / 16;
   pdl_wait();
   pdl_trigger();
   if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -74,10 +82,11 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   const int nunits = (p.k + 31) / 32, step = splits * WARPS, u0 = rank * WARPS + warp;
   const int nchunks = u0 < nunits ? 2 * ((nunits - 1 - u0) / step + 1) : 0;  // of this warp
   const int kv_row = p.Hkv * D;
-  const uint16_t* Kg = p.K + g * D;
-  const uint16_t* Vg = p.V + g * D;
+  // the row's pages on their way to L2 while the positions load
+  for (int i = threadIdx.x * 32; i < min(p.table_width, WARPS * 32 * 32 * 4); i += WARPS * 32 * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(trow + i));
 
-  const int len = __ldg(p.lens + row);
+  const int len = max(__ldg(p.lens + row), 0);
   uint32_t qb[MT][2];
   {
     const int head = lane / 4;
@@ -94,63 +103,77 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   // page -> row is three dependent loads, so a unit's pages are looked up one unit ahead of its
   // copies and its positions two ahead.
   auto position = [&](int u) { return u < nunits && u * 32 + lane < p.k ? __ldg(idx + u * 32 + lane) : -1; };
-  // cache slot (page * P + row in page) of a position, or -1
-  auto cache_slot = [&](int s) {
-    if ((unsigned)s >= (unsigned)max(len, 0)) return -1;
-    const int pg = s >> p.page_shift;
-    if (pg >= p.table_width) return -1;
-    const int page = __ldg(trow + pg);
-    if ((unsigned)page >= (unsigned)p.num_pages) return -1;
-    return (page << p.page_shift) | (s & ((1 << p.page_shift) - 1));
+  // where a position's K and V rows start in the caches (bytes), or -1
+  struct Slot {
+    long long k, v;
   };
-  // starts the copies of a chunk, the lanes' slots from `first` on; returns its mask of valid slots
-  auto issue = [&](int st, int mine, int first) -> uint32_t {
-    const uint32_t kdst = my_s + st * C::STAGE_BYTES, vdst = kdst + TILE_BYTES;
-    const int sub = lane >> 3, c = lane & 7;
+  // (two steps, so that nothing waits between a page's load and its use)
+  auto page_of = [&](int s) {
+    const int pg = s >> p.page_shift;
+    return (unsigned)s < (unsigned)len && pg < p.table_width ? __ldg(trow + pg) : -1;
+  };
+  auto slot_of = [&](int s, int page) -> Slot {
+    if ((unsigned)page >= (unsigned)p.num_pages) return {-1, -1};
+    const long long in = (long long)(s & ((1 << p.page_shift) - 1)) * kv_row;
+    return {2 * (page * p.k_page_stride + in), SAME ? 0 : 2 * (page * p.v_page_stride + in)};
+  };
+  // starts the copies of a chunk, the lanes' slots from `first` on; returns its mask of valid
+  // slots.  Eight lanes per row: each copy instruction moves 128-byte pieces of four rows.
+  const uint32_t dst0 = my_s + (lane >> 3) * C::ROW + (lane & 7) * 16;
+  const char* Kc = reinterpret_cast<const char*>(p.K + g * D) + (lane & 7) * 16;
+  const char* Vc = reinterpret_cast<const char*>(p.V + g * D) + (lane & 7) * 16;
+  auto issue = [&](int st, const Slot& mine, int first) -> uint32_t {
+    const uint32_t vm = (__ballot_sync(0xffffffffu, mine.k >= 0) >> first) & 0xFFFFu;
+    const uint32_t dst = dst0 + st * C::STAGE_BYTES;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = 4 * j + sub;
-      const int cs = __shfl_sync(0xffffffffu, mine, first + r);
-      const bool valid = cs >= 0;
-      const int page = cs >> p.page_shift;
-      const int in = (cs & ((1 << p.page_shift) - 1)) * kv_row + c * 8;
-      const uint16_t* ksrc = valid ? Kg + page * p.k_page_stride + in : Kg;
-      const uint16_t* vsrc = valid ? Vg + page * p.v_page_stride + in : Vg;
-      const uint32_t o = tile_off<D>(r, c);
+      const int r = first + 4 * j + (lane >> 3);
+      const long long ko = __shfl_sync(0xffffffffu, mine.k, r);
+      const long long vo = SAME ? ko : __shfl_sync(0xffffffffu, mine.v, r);
+      if (vm == 0xFFFFu) {
 #pragma unroll
-      for (int h = 0; h < SEGS / 8; ++h) {
-        cp_async_16(kdst + o + h * 128, ksrc + h * 64, valid);
-        cp_async_16(vdst + o + h * 128, vsrc + h * 64, valid);
+        for (int h = 0; h < D / 64; ++h) {
+          cp_async_16_all(dst + j * 4 * C::ROW + h * 128, Kc + ko + h * 128);
+          cp_async_16_all(dst + C::TILE_BYTES + j * 4 * C::ROW + h * 128, Vc + vo + h * 128);
+        }
+      } else {  // slots that do not count are filled with zeros
+        const bool valid = ko >= 0;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          cp_async_16(dst + j * 4 * C::ROW + h * 128, Kc + (valid ? ko : 0) + h * 128, valid);
+          cp_async_16(dst + C::TILE_BYTES + j * 4 * C::ROW + h * 128, Vc + (valid ? vo : 0) + h * 128, valid);
+        }
       }
     }
     cp_async_commit();
-    return (__ballot_sync(0xffffffffu, mine >= 0) >> first) & 0xFFFFu;
+    return vm;
   };
 
+  // ldmatrix addresses of this lane: K rows, and V rows transposed
+  const uint32_t k_lane = my_s + (lane & 15) * C::ROW + (lane >> 4) * 16;
+  const uint32_t v_lane = my_s + C::TILE_BYTES + ((lane & 7) + ((lane >> 4) << 3)) * C::ROW + ((lane >> 3) & 1) * 16;
   float acc[MT][4] = {};
   float m0 = -INFINITY, m1 = -INFINITY;  // running max (log2 domain) of heads h0, h1
-  float l0 = 0.f, l1 = 0.f;              // this lane's share of the sums (for the lse)
-  float r0 = 0.f, r1 = 0.f;              // the same of the bf16-rounded weights that multiply V
+  float l0 = 0.f, l1 = 0.f;              // this lane's share of the sums
 
   uint32_t vmr[STAGES];  // valid masks of the chunks in flight, the next one to use first
-  int cs_cur = -1, cs_next, s_next, u_next = u0 + step;
-  {
-    const int s0 = position(u0), s1 = position(u_next);
-    cs_cur = cache_slot(s0);
-    cs_next = cache_slot(s1);
-    s_next = position(u_next += step);
-  }
+  int u_next = u0 + step;
+  int s_cur = position(u0), s_next = position(u_next);
+  int pg_cur = page_of(s_cur), pg_next = page_of(s_next);
+  int s_far = position(u_next += step);
+  Slot cs = slot_of(s_cur, pg_cur);
   auto issue_chunk = [&](int n) -> uint32_t {
     if (n >= nchunks) {
       cp_async_commit();
       return 0u;
     }
     if (n > 0 && n % 2 == 0) {  // the next unit
-      cs_cur = cs_next;
-      cs_next = cache_slot(s_next);
-      s_next = position(u_next += step);
+      cs = slot_of(s_next, pg_next);
+      s_next = s_far;
+      pg_next = page_of(s_next);
+      s_far = position(u_next += step);
     }
-    return issue(n % STAGES, cs_cur, n % 2 * 16);
+    return issue(n % STAGES, cs, n % 2 * 16);
   };
 #pragma unroll
   for (int j = 0; j < STAGES - 1; ++j) vmr[j] = issue_chunk(j);
@@ -165,14 +188,13 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
 #pragma unroll
     for (int j = 0; j + 1 < STAGES; ++j) vmr[j] = vmr[j + 1];
     if (vm != 0) {  // warp-uniform: chunks of unused slots are passed over
-      const uint32_t kt = my_s + st * C::STAGE_BYTES, vt = kt + TILE_BYTES;
       // ---- S^T = K_chunk . Q^T, two interleaved accumulator chains
       float sa[4] = {}, sb[4] = {};
 #pragma unroll
       for (int kk = 0; kk < MT; kk += 2) {
         uint32_t a0, a1, a2, a3, e0, e1, e2, e3;
-        ldmatrix_x4(kt + tile_off<D>(lane & 15, kk * 2 + (lane >> 4)), a0, a1, a2, a3);
-        ldmatrix_x4(kt + tile_off<D>(lane & 15, (kk + 1) * 2 + (lane >> 4)), e0, e1, e2, e3);
+        ldmatrix_x4(k_lane + st * C::STAGE_BYTES + kk * 32, a0, a1, a2, a3);
+        ldmatrix_x4(k_lane + st * C::STAGE_BYTES + kk * 32 + 32, e0, e1, e2, e3);
         mma_bf16_16816(sa, a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
         mma_bf16_16816(sb, e0, e1, e2, e3, qb[kk + 1][0], qb[kk + 1][1]);
       }
@@ -196,8 +218,6 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
         if (up1) m1 = cm1;
         l0 *= al0;
         l1 *= al1;
-        r0 *= al0;
-        r1 *= al1;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           acc[mt][0] *= al0;
@@ -211,18 +231,19 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
       const float p10 = exp2f(x10 - mu0), p11 = exp2f(x11 - mu1);
       l0 += p00 + p10;
       l1 += p01 + p11;
-      // P is rounded to bf16 for the product; O is divided by the sum of the rounded weights
-      const uint32_t pk0 = pack_bf16x2(p00, p01), pk1 = pack_bf16x2(p10, p11);
-      r0 += __uint_as_float(pk0 << 16) + __uint_as_float(pk1 << 16);
-      r1 += __uint_as_float(pk0 & 0xFFFF0000u) + __uint_as_float(pk1 & 0xFFFF0000u);
-      // ---- O^T += V^T . P^T
-      const uint32_t pb0 = movmatrix_trans(pk0), pb1 = movmatrix_trans(pk1);
-      const int vrow = (lane & 7) + ((lane >> 4) << 3), vseg_off = (lane >> 3) & 1;
+      // ---- O^T += V^T . P^T, each weight as two bf16 (what the first rounds off is the second, so
+      // 2^-16 of a weight is lost, not 2^-8); V's fragments serve both products
+      const uint32_t hi0 = pack_bf16x2(p00, p01), hi1 = pack_bf16x2(p10, p11);
+      const uint32_t lo0 = pack_bf16x2(p00 - __uint_as_float(hi0 << 16), p01 - __uint_as_float(hi0 & 0xFFFF0000u));
+      const uint32_t lo1 = pack_bf16x2(p10 - __uint_as_float(hi1 << 16), p11 - __uint_as_float(hi1 & 0xFFFF0000u));
+      const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
+      const uint32_t c0 = movmatrix_trans(lo0), c1 = movmatrix_trans(lo1);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         uint32_t a0, a1, a2, a3;
-        ldmatrix_x4_trans(vt + tile_off<D>(vrow, mt * 2 + vseg_off), a0, a1, a2, a3);
-        mma_bf16_16816(acc[mt], a0, a1, a2, a3, pb0, pb1);
+        ldmatrix_x4_trans(v_lane + st * C::STAGE_BYTES + mt * 32, a0, a1, a2, a3);
+        mma_bf16_16816(acc[mt], a0, a1, a2, a3, b0, b1);
+        mma_bf16_16816(acc[mt], a0, a1, a2, a3, c0, c1);
       }
     }
     __syncwarp();  // stage st is refilled by the next iteration's copies
@@ -235,14 +256,12 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   for (int o = 4; o < 32; o <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, o);
     l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-    r0 += __shfl_xor_sync(0xffffffffu, r0, o);
-    r1 += __shfl_xor_sync(0xffffffffu, r1, o);
   }
   const int h0 = 2 * (lane % 4);
-  float4* s_ml = reinterpret_cast<float4*>(smem + C::OFF_ML);
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
   if (lane < 4) {
-    s_ml[warp * 8 + h0] = make_float4(m0, l0, r0, 0.f);
-    s_ml[warp * 8 + h0 + 1] = make_float4(m1, l1, r1, 0.f);
+    s_ml[warp * 8 + h0] = make_float2(m0, l0);
+    s_ml[warp * 8 + h0 + 1] = make_float2(m1, l1);
   }
   float* wo = reinterpret_cast<float*>(my);
 #pragma unroll
@@ -255,63 +274,79 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   }
   __syncthreads();
 
-  // ---- the block's state, sent to the blocks that finish the outputs: output e belongs to
-  // block e % splits.  Every block of the cluster has started (the barrier's first phase).
+  // ---- the block's state, four dims of a head per thread, sent to the block that finishes them:
+  // the G D / 4 pieces are dealt to the cluster's blocks (a power of two of them) in order.
+  // Every block has started by then (the barrier's first phase).
   cg::cluster_group cluster = cg::this_cluster();
-  float* s_co = reinterpret_cast<float*>(smem + C::OFF_CO);
-  float4* s_cml = reinterpret_cast<float4*>(smem + C::OFF_CML);
-  const int share = (8 * D + splits - 1) / splits;
-  if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  for (int e = threadIdx.x; e < p.G * D; e += WARPS * 32) {
-    const int h = e / D;
-    float M = -INFINITY;
+  float4* s_co = reinterpret_cast<float4*>(smem + C::OFF_CO);
+  float2* s_cml = reinterpret_cast<float2*>(smem + C::OFF_CML);
+  const int pieces = p.G * D / 4, share_log = 31 - __clz(pieces / splits);
+  const long long head0 = row * p.Hq + g * p.G;
+  // joins n states (max, sum) and O pieces, given by get(i, state, piece), in order
+  auto join = [&](auto n, auto&& get, float& M, float& L, float4& o) {
+    float2 ml[n.value];
+    float4 x[n.value];
+    M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w * 8 + h].x);
-    const float mu = M == -INFINITY ? 0.f : M;
-    float o = 0.f, L = 0.f, R = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float4 ml = s_ml[w * 8 + h];
-      const float f = exp2f(ml.x - mu);  // a warp without keys: 2^-inf = 0
-      L = fmaf(ml.y, f, L);
-      R = fmaf(ml.z, f, R);
-      o = fmaf(reinterpret_cast<const float*>(smem + w * STAGES * C::STAGE_BYTES)[e], f, o);
+    for (int i = 0; i < n.value; ++i) {
+      get(i, ml[i], x[i]);
+      M = fmaxf(M, ml[i].x);
     }
+    const float mu = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < n.value; ++i) {
+      const float f = exp2f(ml[i].x - mu);  // no keys: 2^-inf = 0
+      L = fmaf(ml[i].y, f, L);
+      o.x = fmaf(x[i].x, f, o.x);
+      o.y = fmaf(x[i].y, f, o.y);
+      o.z = fmaf(x[i].z, f, o.z);
+      o.w = fmaf(x[i].w, f, o.w);
+    }
+  };
+  auto finish = [&](int v, float M, float L, const float4& o) {
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const int h = v / (D / 4);
+    *reinterpret_cast<uint2*>(p.O + head0 * D + v * 4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (p.lse && v % (D / 4) == 0) p.lse[head0 + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  };
+  if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int v = threadIdx.x; v < pieces; v += WARPS * 32) {
+    const int h = v / (D / 4);
+    float M, L;
+    float4 o;
+    join(std::integral_constant<int, WARPS>(),
+         [&](int w, float2& ml, float4& x) {
+           ml = s_ml[w * 8 + h];
+           x = reinterpret_cast<const float4*>(smem + w * STAGES * C::STAGE_BYTES)[v];
+         },
+         M, L, o);
     if (splits == 1) {
-      const long long head = row * p.Hq + g * p.G + h;
-      p.O[head * D + e % D] = __bfloat16_as_ushort(__float2bfloat16_rn(R > 0.f ? o / R : 0.f));
-      if (p.lse && e % D == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+      finish(v, M, L, o);
     } else {
-      cluster.map_shared_rank(s_co, e % splits)[rank * share + e / splits] = o;
-      if (e % D < splits) cluster.map_shared_rank(s_cml, e % D)[rank * 8 + h] = make_float4(M, L, R, 0.f);
+      const int owner = v >> share_log;
+      cluster.map_shared_rank(s_co, owner)[(rank << share_log) + (v & ((1 << share_log) - 1))] = o;
+      if (v % (D / 4) < splits) cluster.map_shared_rank(s_cml, v % (D / 4))[rank * 8 + h] = make_float2(M, L);
     }
   }
   if (splits == 1) return;  // block-uniform
 
-  // ---- over the cluster: this block's outputs from every block's share, in order
+  // ---- over the cluster: this block's pieces from every block's state, in order
   cluster.sync();
-  for (int e = rank + threadIdx.x * splits; e < p.G * D; e += WARPS * 32 * splits) {
-    const int h = e / D;
-    float m[SAP_MAX_SPLITS], M = -INFINITY;
-#pragma unroll
-    for (int q = 0; q < SAP_MAX_SPLITS; ++q) {
-      m[q] = q < splits ? s_cml[q * 8 + h].x : -INFINITY;
-      M = fmaxf(M, m[q]);
-    }
-    const float mu = M == -INFINITY ? 0.f : M;
-    float o = 0.f, L = 0.f, R = 0.f;
-#pragma unroll
-    for (int q = 0; q < SAP_MAX_SPLITS; ++q) {
-      if (q >= splits) continue;
-      const float4 ml = s_cml[q * 8 + h];
-      const float f = exp2f(m[q] - mu);
-      L = fmaf(ml.y, f, L);
-      R = fmaf(ml.z, f, R);
-      o = fmaf(s_co[q * share + e / splits], f, o);
-    }
-    const long long head = row * p.Hq + g * p.G + h;
-    p.O[head * D + e % D] = __bfloat16_as_ushort(__float2bfloat16_rn(R > 0.f ? o / R : 0.f));
-    if (p.lse && e % D == 0) p.lse[head] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  for (int i = threadIdx.x; i < 1 << share_log; i += WARPS * 32) {
+    const int v = (rank << share_log) + i, h = v / (D / 4);
+    float M, L;
+    float4 o;
+    join(std::integral_constant<int, SAP_MAX_SPLITS>(),
+         [&](int q, float2& ml, float4& x) {
+           const bool in = q < splits;
+           ml = in ? s_cml[q * 8 + h] : make_float2(-INFINITY, 0.f);
+           x = in ? s_co[(q << share_log) + i] : make_float4(0.f, 0.f, 0.f, 0.f);
+         },
+         M, L, o);
+    finish(v, M, L, o);
   }
 }
 
@@ -319,10 +354,10 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
 
 namespace dsa_host {
 
-template <int D, int WARPS>
-static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int splits, bool pdl, cudaStream_t stream) {
+template <int D, int WARPS, bool SAME>
+static int sa_paged_launch_same(const dsa::SAPagedParams& p, long long groups, int splits, bool pdl, cudaStream_t stream) {
   constexpr int STAGES = 2;
-  auto kern = dsa::sparse_attn_paged_kernel<D, WARPS, STAGES>;
+  auto kern = dsa::sparse_attn_paged_kernel<D, WARPS, STAGES, SAME>;
   const int smem = dsa::SAPagedSmem<D, WARPS, STAGES>::BYTES;
   static DeviceFlag done;
   if (!done) {
@@ -352,6 +387,12 @@ static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int 
   cfg.numAttrs = n;
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, splits); e != cudaSuccess) return cuda_fail(e);
   return last_launch_status();
+}
+
+template <int D, int WARPS>
+static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int splits, bool pdl, cudaStream_t stream) {
+  return p.k_page_stride == p.v_page_stride ? sa_paged_launch_same<D, WARPS, true>(p, groups, splits, pdl, stream)
+                                            : sa_paged_launch_same<D, WARPS, false>(p, groups, splits, pdl, stream);
 }
 
 // While the (row, KV head) groups do not fill the SMs, blocks of 8 warps, one per SM, and the
