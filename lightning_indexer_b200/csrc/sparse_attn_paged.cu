@@ -395,20 +395,25 @@ static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int 
                                             : sa_paged_launch_same<D, WARPS, false>(p, groups, splits, pdl, stream);
 }
 
-// While the (row, KV head) groups do not fill the SMs, blocks of 8 warps, one per SM, and the
-// largest cluster that still gives every block an SM of its own and every warp a unit; past
-// that, blocks of 4 warps without clusters.  Joining over a cluster costs about 2.5 us and a
-// block's start as much again, so more and smaller pieces lose: 16 sequences of 2048 slots
-// (64 groups) take 19.5 us as clusters of 2, 29 as clusters of 8; 64 sequences 48 us unsplit
-// with 4 warps, 53 with 8, 58 as clusters of 2.
+// While the (row, KV head) groups do not fill the SMs: blocks of 8 warps, one per SM, in the
+// largest cluster that still gives every block an SM of its own and every warp a unit, or of 4
+// warps where those already give every unit its warp.  Past that, blocks of 4 warps, three per
+// SM, without clusters.  Joining over a cluster costs about 1.5 us, so more and smaller pieces
+// lose: 16 sequences of 2048 slots (64 groups) take 17.0 us as clusters of 2, 17.5 as clusters
+// of 4 blocks of 4 warps, 22 and more as clusters of 8; 7 of 512 slots 6.1 us with 4 warps, 7.1
+// with 8; 64 of 2048 47 us unsplit with 4 warps, 50 with 8, 54 and more as clusters.
 template <int D>
 static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, cudaStream_t stream) {
-  const long long groups = (long long)batch * p.Hkv;
-  const int sms = sm_count();
+  const long long groups = (long long)batch * p.Hkv, sms = sm_count();
   if (groups > sms) return sa_paged_launch_t<D, 4>(p, groups, 1, pdl, stream);
-  int splits = 1;
-  while (splits < dsa::SAP_MAX_SPLITS && groups * splits * 2 <= sms && splits * 2 * 8 * 32 <= p.k) splits *= 2;
-  return sa_paged_launch_t<D, 8>(p, groups, splits, pdl, stream);
+  const int units = (p.k + 31) / 32;
+  auto splits = [&](int warps) {
+    int n = 1;
+    while (n < dsa::SAP_MAX_SPLITS && groups * n * 2 <= sms && n * 2 * warps <= units) n *= 2;
+    return n;
+  };
+  if (splits(4) * 4 >= units) return sa_paged_launch_t<D, 4>(p, groups, splits(4), pdl, stream);
+  return sa_paged_launch_t<D, 8>(p, groups, splits(8), pdl, stream);
 }
 
 int sparse_attn_paged_launch(const dsa::SAPagedParams& p, int batch, int d, bool pdl, cudaStream_t stream) {

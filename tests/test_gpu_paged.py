@@ -485,6 +485,44 @@ def test_decode_step_graph_two_streams():
     assert dsa.device_status() == (0, 0)
 
 
+def test_capture_with_a_second_stream():
+    """A captured region in which a call's inputs come from another stream, and the call's outputs go
+    back to it, replays as it ran."""
+    g = torch.Generator().manual_seed(23)
+    page, Hq, Hkv, d, k, lens = 16, 8, 2, 64, 64, [200, 77, 150]
+    Q, kc, vc, idx, table, _ = make_attention_case(Hq, Hkv, d, k, page, lens, 23)
+    x, w, f = randn(3, Hq, d, gen=g).cuda(), weight(d, g).cuda(), ref.frequencies(d).cuda()
+    kc, vc, idx, table, n = kc.cuda(), vc.cuda(), idx.cuda(), table.cuda(), i32(lens).cuda()
+    cu = torch.arange(4, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            q, _ = dsa.norm_rope(x * 2, None, w, None, f, cu_seqlens_q=cu, seqlens_k=n)
+        main.wait_stream(side)
+        O, lse = dsa.sparse_attn_decode_paged(q, kc, vc, idx, table, n)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            y, _ = dsa.norm_rope(O, None, w)
+        main.wait_stream(side)
+        return q, O, lse, y
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for seed in (1, 2, 3):
+        x.copy_(randn(3, Hq, d, gen=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_binding_checks_sizes():
     """Sizes that would make a kernel read past a tensor are refused before anything is enqueued."""
     z = lambda *s, t=BF16: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
