@@ -233,6 +233,10 @@ struct LaneTurns {
   F2 c[4], s[4];
 };
 
+// Where the turn of frequency f lies in the exchange buffer: two to a 16-byte piece, the pieces
+// that a row's lanes read together side by side.
+__device__ __forceinline__ int cs_slot(int f) { return (((f >> 1) & 3) * 8 + (f >> 3)) * 2 + (f & 1); }
+
 // This lane's turns at its row's position.  Where every row of the warp belongs to one token,
 // the lanes compute the token's rotary / 2 pairs side by side and exchange them through
 // shared memory.
@@ -245,11 +249,11 @@ __device__ __forceinline__ void lane_turns(const HeadSeg& s, const LaneCols<D, I
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < (D + 63) / 64; ++j)
-      if (32 * j + lane < s.rotary / 2) turn(angle_at(ts.step[32 * j + lane], pos), cs[32 * j + lane].x, cs[32 * j + lane].y);
+      if (const int f = 32 * j + lane; f < s.rotary / 2) turn(angle_at(ts.step[f], pos), cs[cs_slot(f)].x, cs[cs_slot(f)].y);
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < 8; p += 2) {
-      const float4 v = FULL || col.rotates(p) ? *reinterpret_cast<const float4*>(cs + col.freq(p)) : make_float4(1.f, 0.f, 1.f, 0.f);
+      const float4 v = FULL || col.rotates(p) ? *reinterpret_cast<const float4*>(cs + cs_slot(col.freq(p))) : make_float4(1.f, 0.f, 1.f, 0.f);
       L.c[p / 2] = f2(v.x, v.z);
       L.s[p / 2] = f2(v.y, v.w);
     }
@@ -693,11 +697,11 @@ static long long seg_groups(const dsa::HeadRowsParams& p, const dsa::HeadSeg& s)
 // cost about 4 and are paid once per token and run.
 static int group_weight(const dsa::HeadSeg& s) { return 10 + 4 * (512 / s.D) / std::max(s.heads, 512 / s.D); }
 
-// Fills in what the kernels read of each segment: runs of up to `run` groups, dealt to about
-// `warps` warps in all, to the tensors by their cost (0: a warp for each run).  Returns the
-// number of blocks.
-static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps, int block_warps) {
-  long long cost = 1, block = 0;
+// Fills in what the kernels read of each segment: runs of up to `run` groups, dealt to `total`
+// blocks in all, to the tensors by their cost (0: a warp for each run).  Returns the number of
+// blocks.
+static int plan_segs(dsa::HeadRowsParams& p, int run, long long total, int block_warps) {
+  long long cost = 0, block = 0;
   for (int i = 0; i < p.nseg; ++i) cost += seg_groups(p, p.seg[i]) * group_weight(p.seg[i]);
   for (int i = 0; i < p.nseg; ++i) {
     dsa::HeadSeg& s = p.seg[i];
@@ -711,8 +715,11 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, long long warps, int block
     s.div_mul = (unsigned)(((1ULL << (31 + lg)) + s.heads - 1) / s.heads);
     s.block0 = (int)block;
     const long long nruns = ((long long)s.groups + s.iters - 1) / s.iters;
-    const long long share = warps ? (warps * s.groups * group_weight(s) + cost - 1) / cost : nruns;
-    const long long blocks = (std::min(nruns, std::max<long long>(share, 1)) + block_warps - 1) / block_warps;
+    const long long most = (nruns + block_warps - 1) / block_warps, mine = s.groups * (long long)group_weight(s);
+    // the nearest share of what is left, which the last tensor takes whole
+    const long long share = total ? ((total - block) * mine + cost / 2) / std::max<long long>(cost, 1) : most;
+    const long long blocks = std::min(most, std::max<long long>(share, 1));
+    cost -= mine;
     s.warps = (int)(blocks * block_warps);
     block += blocks;
   }
@@ -740,14 +747,15 @@ int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) 
   return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_FWD_WARPS * 32), 0, stream, p);
 }
 
-// Blocks of the backward: one wave, at most 16 warps per SM, since each block adds a share to
+// Blocks of the backward: one wave, two blocks on every SM, since each block adds a share to
 // the weights' gradients.  They set the order of those sums and the size of the workspace, so
 // they follow from the sizes alone.
 static int bwd_plan(dsa::HeadRowsParams& p) {
-  const long long warps = 15LL * sm_count();  // the last block of a tensor may be part empty
+  const long long blocks = 2LL * sm_count();
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
-  return plan_segs(p, (int)std::max<long long>(1, std::min<long long>(8, groups / warps)), warps, dsa::NR_BWD_WARPS);
+  const int run = (int)std::max<long long>(1, std::min<long long>(8, groups / (blocks * dsa::NR_BWD_WARPS)));
+  return plan_segs(p, run, blocks, dsa::NR_BWD_WARPS);
 }
 size_t norm_rope_bwd_ws_bytes(long long T, int Hq, int Hk, int d) {
   dsa::HeadRowsParams p{};
