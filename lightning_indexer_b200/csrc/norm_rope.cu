@@ -428,7 +428,7 @@ __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const Hea
   unpack8(gb, g1);
   load_steps(s, ts);
   LaneTurns turns;
-#pragma unroll 1
+#pragma unroll 2
   for (int it = 0; it < n; ++it) {
     issue();
     const bool in = SHARED || at.r < row_end;
@@ -548,7 +548,7 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
   LaneTurns turns;
   RunPlaces all, cur;
   int cur_t = -1, t_first = 0;
-#pragma unroll 1
+#pragma unroll 2
   for (int it = 0; it < n; ++it) {
     if (at.left == s.iters)  // a new run's tokens
       t_first = runs_look_up(p.tk, s, all, at.r - rg, n - it, L::RPW, rows, lane), cur_t = -1;
