@@ -10,7 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/full.h>
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -54,6 +54,11 @@ const char* type_text(at::ScalarType t) {
 }
 
 using Shape = std::initializer_list<int64_t>;
+
+// An uninitialised tensor on `like`'s device, without the dispatcher (half the cost).
+Tensor new_tensor(Shape shape, at::ScalarType type, const Tensor& like) {
+  return at::detail::empty_cuda(at::IntArrayRef(shape), type, like.device(), std::nullopt);
+}
 
 const Tensor& tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
@@ -250,8 +255,8 @@ PyObject* norm_rope(PyObject* const* a) {
     Qo = *x;
     if (has_k) Ko = *y;
   } else {
-    Qo = at::empty({T, Hq, d}, Q.options());
-    if (has_k) Ko = at::empty({T, Hk, d}, Q.options());
+    Qo = new_tensor({T, Hq, d}, at::kBFloat16, Q);
+    if (has_k) Ko = new_tensor({T, Hk, d}, at::kBFloat16, Q);
   }
   void* qo = c.rows(Qo, "Q out", {T, Hq, d}, &qos);
   if (has_k) ko = c.rows(Ko, "K out", {T, Hk, d}, &kos);
@@ -293,24 +298,24 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
     dQ = *x;
     if (has_k) dK = *y;
   } else {
-    dQ = at::empty({T, Hq, d}, Q.options());
-    if (has_k) dK = at::empty({T, Hk, d}, Q.options());
+    dQ = new_tensor({T, Hq, d}, at::kBFloat16, Q);
+    if (has_k) dK = new_tensor({T, Hk, d}, at::kBFloat16, Q);
   }
   void* dq = c.rows(dQ, "dQ", {T, Hq, d}, &dqs);
   if (has_k) dk = c.rows(dK, "dK", {T, Hk, d}, &dks);
-  const auto f32 = Q.options().dtype(at::kFloat);
   if (T == 0) {
+    const auto f32 = Q.options().dtype(at::kFloat);
     if (gq) dgq = at::zeros({d}, f32);
     if (gk) dgk = at::zeros({d}, f32);
     return pack(dQ, dK, dgq, dgk);
   }
-  if (gq) dgq = at::empty({d}, f32);
-  if (gk) dgk = at::empty({d}, f32);
+  if (gq) dgq = new_tensor({d}, at::kFloat, Q);
+  if (gk) dgk = new_tensor({d}, at::kFloat, Q);
   if (a[13] != Py_None) {
     ws = tensor(a[13], "workspace");
     c.dense(ws, "workspace", at::kByte, {ws.numel()});
   } else if (gq || gk) {
-    ws = at::empty({(int64_t)dsa_norm_rope_bwd_workspace_size(T, (int)Hq, (int)Hk, (int)d)}, Q.options().dtype(at::kByte));
+    ws = new_tensor({(int64_t)dsa_norm_rope_bwd_workspace_size(T, (int)Hq, (int)Hk, (int)d)}, at::kByte, Q);
   }
   launch(c, "dsa_norm_rope_bwd", [&](void* st) {
     return dsa_norm_rope_bwd(q, qs, k, ks, dqo, dqos, dko, dkos, gq, gk, eps, rope.freq, rope.rotary, inter, tk.positions,
@@ -407,9 +412,9 @@ struct DecodeOut {
       }
       return;
     }
-    O = at::empty({B, Hq, d}, Q.options());
-    lse = at::empty({B, Hq}, Q.options().dtype(at::kFloat));
-    if (with_indices) indices = at::empty({B, k > 0 ? k : 0}, Q.options().dtype(at::kInt));
+    O = new_tensor({B, Hq, d}, at::kBFloat16, Q);
+    lse = new_tensor({B, Hq}, at::kFloat, Q);
+    if (with_indices) indices = new_tensor({B, k > 0 ? k : 0}, at::kInt, Q);
   }
   float* lse_ptr() const { return lse.defined() ? lse.data_ptr<float>() : nullptr; }
 };
@@ -437,7 +442,7 @@ PyObject* sparse_attn_decode_paged(PyObject* const* a) {
 }
 
 Tensor workspace(Call& c, PyObject* o, size_t bytes, const Tensor& like) {
-  if (o == Py_None) return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+  if (o == Py_None) return new_tensor({(int64_t)bytes}, at::kByte, like);
   const Tensor& t = tensor(o, "workspace");
   c.dense(t, "workspace", at::kByte, {t.numel()});
   return t;

@@ -124,6 +124,10 @@ __global__ void __launch_bounds__(224, 1)
   pdl_wait();
   pdl_trigger();
 
+  // the table on its way to L2 while the lengths load (the first 128 bytes per thread of the grid)
+  if (const long long at = ((long long)blockIdx.x * C::THREADS + threadIdx.x) * 32; at < (long long)p.batch * p.table_width)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + at));
+
   // ---- the list of tiles: thread i sums a run of sequences, the block scans the sums
   long long first, count;
   {
