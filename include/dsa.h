@@ -440,7 +440,8 @@ DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int
  * receives position s's score, -inf on a page that is not there; the rest is untouched.
  * (Several query rows of one sequence, as when drafted tokens are checked, are entries of
  * their own with the same table row and growing lengths.)
- * Supported: the (H_I, d_I) of (1).
+ * ld_scores >= max_seqlen_k and a multiple of 4.
+ * Supported: the (H_I, d_I) of (1); batch * H_I < 2^31; max_seqlen_k < 2^31 - 1024.
  * ------------------------------------------------------------------------------- */
 DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t k_idx_page_stride,
                             const void* w, const int32_t* block_table, int max_pages,
@@ -454,7 +455,7 @@ DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t 
  * an empty set gives O = 0 and lse = -inf.  One launch and no workspace.  Two equal entries
  * of a row count twice, as in (3).  Repeats of a call are bit-identical; how a row's slots are
  * split over blocks depends on the batch, so a row's last bits may differ between batches.
- * Supported: the shapes of (4).
+ * Supported: the shapes of (4); page_size * Hkv * d < 2^31.
  * ------------------------------------------------------------------------------- */
 DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int64_t k_page_stride,
                                          const void* v_cache, int64_t v_page_stride,
@@ -465,7 +466,9 @@ DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int
 
 /* ---------------------------------------------------------------------------------
  * (7c) Whole DSA decode step over the paged cache: (7a), (2), then (7b), on a cache that
- * holds the current token already.  indices device int32 [batch, k] receives the sets.
+ * holds the current token already.  indices device int32 [batch, k] receives the sets
+ * (positions on pages that are not there come last, where fewer than k others are seen; the
+ * attention ignores them).
  *   workspace: dsa_decode_paged_workspace_size(batch, max_seqlen_k) bytes.
  * Supported: the shapes of (7a) and (7b); batch * max_seqlen_k < 2^31.
  * ------------------------------------------------------------------------------- */

@@ -134,6 +134,7 @@ static int index_paged_args_status(const void* q_idx, const void* k_cache, int64
   if (!pool_ok(k_cache, page_stride, (int64_t)page_size * d_I)) return DSA_ERR_INVALID_ARG;
   if (st != DSA_OK) return st;
   if (!index_shape_supported(H_I, d_I) || (int64_t)batch * H_I > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED;
+  if (max_seqlen_k > 0x7FFFFFFF - 1024) return DSA_ERR_UNSUPPORTED;  // positions a few tiles past the end stay ints
   return DSA_OK;
 }
 

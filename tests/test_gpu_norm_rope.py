@@ -118,7 +118,7 @@ def test_special_values():
 
 
 @pytest.mark.parametrize("T,Hq,Hk,d,rotary,inter", SHAPES)
-@pytest.mark.parametrize("norm", [(True, True), (True, False), (False, False)])
+@pytest.mark.parametrize("norm", [(True, True), (True, False), (False, True), (False, False)])
 def test_backward(T, Hq, Hk, d, rotary, inter, norm):
     g = torch.Generator().manual_seed(T * 11 + d)
     Q, K = randn(T, Hq, d, gen=g, scale=2.0), randn(T, Hk, d, gen=g, scale=0.1)

@@ -27,7 +27,7 @@ ROPE_CASES = [
     (dict(ks=504), BAD_ARG), (dict(eps=-1.0), BAD_ARG), (dict(eps=float("nan")), BAD_ARG), (dict(rotary=0), BAD_ARG),
     (dict(freq=None), BAD_ARG), (dict(rotary=144), BAD_ARG), (dict(rotary=-16), BAD_ARG), (dict(cu=None), BAD_ARG), (dict(batch=0), BAD_ARG),
     (dict(cu=None, batch=1, lens=FAKE), BAD_ARG), (dict(rotary=24), UNSUPPORTED), (dict(d=96, rotary=96), UNSUPPORTED),
-    (dict(T=1 << 27), UNSUPPORTED), (dict(T=0), 0)]
+    (dict(T=1 << 27), UNSUPPORTED), (dict(qs=1 << 31), BAD_ARG), (dict(T=0), 0)]
 
 
 def test_norm_rope_refusals():
@@ -75,7 +75,7 @@ def test_index_paged_refusals():
                 scores=FAKE, ld=128)
     cases = POOL_CASES + [(dict(q=None), BAD_ARG), (dict(w=MIS), BAD_ARG), (dict(ic=None), BAD_ARG), (dict(ics=16 * 128 - 8), BAD_ARG),
                           (dict(maxk=-1), BAD_ARG), (dict(scores=None), BAD_ARG), (dict(scores=MIS), BAD_ARG), (dict(ld=124), BAD_ARG),
-                          (dict(ld=130), BAD_ARG), (dict(H_I=48), UNSUPPORTED), (dict(d_I=64), UNSUPPORTED)]
+                          (dict(ld=130), BAD_ARG), (dict(maxk=0x7FFFFFFF, ld=1 << 31), UNSUPPORTED), (dict(H_I=48), UNSUPPORTED), (dict(d_I=64), UNSUPPORTED)]
     refused("dsa_index_paged", base, list(base), cases)
 
 
