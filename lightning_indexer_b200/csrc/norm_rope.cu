@@ -20,6 +20,12 @@
 // memory by asynchronous copies (no registers held while they fly), and the places of the
 // run's tokens (sequence, position, page) are looked up by its lanes side by side, one chain
 // of dependent loads per run instead of one per group.
+//
+// Bound by HBM (4 bytes an element forward, 6 backward) with the issue slots close behind:
+// about 210 instructions a group of 1 KiB forward, 300 backward.  Measured: 32768 tokens of
+// 32 + 4 heads of 128 in 96 to 103 us (6.2 to 5.9 TB/s), the backward of 65536 in 303 to 320 us
+// (6.0 to 5.7 TB/s), an append of 32768 tokens (4 + 4 heads and the indexer's key) in 30 us
+// (5.0 TB/s: every group of K is another token, whose turns it computes for itself).
 #include <algorithm>
 
 #include "common.cuh"
