@@ -127,3 +127,12 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         dsa.sparse_attn_decode_paged(x, cache, cache, torch.zeros((2, 16), dtype=torch.int32), table, lens)
     with pytest.raises(ValueError, match="CUDA"):
         dsa.index_paged(x, cache[:, :, 0], torch.zeros((2, 4), dtype=torch.bfloat16), table, lens, 16)
+
+
+def test_missing_native_binding_fails_loudly(monkeypatch):
+    import sys
+    monkeypatch.setattr(dsa, "_native_module", None)
+    monkeypatch.delattr(dsa, "_binding", raising=False)
+    monkeypatch.setitem(sys.modules, "lightning_indexer_b200._binding", None)
+    with pytest.raises(ImportError):
+        dsa.norm_rope(torch.zeros((1, 1, 32), dtype=torch.bfloat16))
