@@ -284,8 +284,9 @@ DSA_API int dsa_norm_rope(const void* Q, int64_t q_stride, const void* K, int64_
   dsa::HeadRowsParams p{};
   p.eps = eps;
   p.tk = token_map(positions, cu_seqlens_q, seqlens_k, batch, total_q);
-  p.seg[p.nseg++] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, Q_out, q_out_stride);
+  // K's few heads per token cost more per row: they go first
   if (K) p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, K_out, k_out_stride);
+  p.seg[p.nseg++] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, Q_out, q_out_stride);
   return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
 }
 
