@@ -67,7 +67,7 @@ struct TileWalk {
   int b, t, len;
   __device__ __forceinline__ int length(int i) const {
     const long long cap = min((long long)p.max_len, (long long)p.table_width << p.page_shift);
-    return (int)min((long long)max(__ldg(p.lens + i), 0), cap);
+    return (int)min((long long)max(p.lens[i], 0), cap);
   }
   __device__ __forceinline__ TileWalk(const IndexPagedParams& q, long long n, int b0, int t0) : p(q), left(n), b(b0), t(t0) {
     len = left > 0 ? length(b) : 0;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(224, 1)
     tmem_alloc(tmem_holder, C::TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();
+  pdl_wait();  // (loads below are plain: a read-only load may be moved above the wait)
   pdl_trigger();
 
   // the table on its way to L2 while the lengths load (the first 128 bytes per thread of the grid)
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(224, 1)
       // and looked at only when used: a lookup per tile put a memory latency into every tile.
       auto pages_from = [&](int q) {
         const long long s = (long long)(q + lane) * box_rows;
-        return s < w.len ? __ldg(row + (int)(s >> p.page_shift)) : -1;
+        return s < w.len ? row[s >> p.page_shift] : -1;
       };
       int q0 = w.t * pieces, ids = pages_from(q0), ids_next = pages_from(q0 + 32);
       if (producer == 0 && lane == 0) {
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(224, 1)
       float wr[H_I];
 #pragma unroll
       for (int h = 0; h < H_I; h += 4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.w + (long long)w.b * H_I + h));
+        const uint2 v = *reinterpret_cast<const uint2*>(p.w + (long long)w.b * H_I + h);
         wr[h] = __uint_as_float(v.x << 16);
         wr[h + 1] = __uint_as_float(v.x & 0xffff0000u);
         wr[h + 2] = __uint_as_float(v.y << 16);
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(224, 1)
       const int* row = p.table + (long long)w.b * p.table_width;
       float* out = p.scores + (long long)w.b * p.ld;
       const int end = w.t + w.here();
-      auto page_at = [&](int s) { return s < w.len ? __ldg(row + (s >> p.page_shift)) : -1; };
+      auto page_at = [&](int s) { return s < w.len ? row[s >> p.page_shift] : -1; };
       int id_next = page_at(w.t * 128 + lane_grp * 32 + lane);
       for (int t = w.t; t < end; ++t) {
         const int s = t * 128 + lane_grp * 32 + lane;

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   namespace cg = cooperative_groups;
   using C = SAPagedSmem<D, WARPS, STAGES>;
   constexpr int MT = D / 16;
-  pdl_wait();
+  pdl_wait();  // (loads below are plain: a read-only load may be moved above the wait)
   pdl_trigger();
   if (splits > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   extern __shared__ __align__(128) uint8_t smem[];
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   for (int i = threadIdx.x * 32; i < min(p.table_width, WARPS * 32 * 32 * 4); i += WARPS * 32 * 32)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(trow + i));
 
-  const int len = max(__ldg(p.lens + row), 0);
+  const int len = max(p.lens[row], 0);
   uint32_t qb[MT][2];
   {
     const int head = lane / 4;
@@ -99,15 +99,15 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
     const uint32_t* qrow = reinterpret_cast<const uint32_t*>(p.Q + ((size_t)row * p.Hq + g * p.G + (hv ? head : 0)) * D);
 #pragma unroll
     for (int kk = 0; kk < MT; ++kk) {
-      qb[kk][0] = hv ? __ldg(qrow + kk * 8 + (lane % 4)) : 0u;
-      qb[kk][1] = hv ? __ldg(qrow + kk * 8 + 4 + (lane % 4)) : 0u;
+      qb[kk][0] = hv ? qrow[kk * 8 + (lane % 4)] : 0u;
+      qb[kk][1] = hv ? qrow[kk * 8 + 4 + (lane % 4)] : 0u;
     }
   }
 
   // Slots are handled 32 at a time, a unit, one per lane: two chunks.  The chain position ->
   // page -> row is three dependent loads, so a unit's pages are looked up one unit ahead of its
   // copies and its positions two ahead.
-  auto position = [&](int u) { return u < nunits && u * 32 + lane < p.k ? __ldg(idx + u * 32 + lane) : -1; };
+  auto position = [&](int u) { return u < nunits && u * 32 + lane < p.k ? idx[u * 32 + lane] : -1; };
   // where a position's K and V rows start in the caches (bytes), or -1
   struct Slot {
     long long k, v;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
   // (two steps, so that nothing waits between a page's load and its use)
   auto page_of = [&](int s) {
     const int pg = s >> p.page_shift;
-    return (unsigned)s < (unsigned)len && pg < p.table_width ? __ldg(trow + pg) : -1;
+    return (unsigned)s < (unsigned)len && pg < p.table_width ? trow[pg] : -1;
   };
   auto slot_of = [&](int s, int page) -> Slot {
     if ((unsigned)page >= (unsigned)p.num_pages) return {-1, -1};

@@ -226,3 +226,24 @@ def test_graph_and_streams():
             got.append([dsa.norm_rope_bwd(x, None, dy, None, w, None, freq) for _ in range(8)])
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for runs in got for r in runs for a, b in ((r[0], want[0]), (r[2], want[2])))
+
+
+def test_dependent_calls_back_to_back():
+    """A chain of calls, each on the last one's output, gives what it gives with the device waited for
+    after every call."""
+    g = torch.Generator().manual_seed(10)
+    T, H, d = 2500, 8, 128
+    x, w, f = randn(T, H, d, gen=g).cuda(), weight(d, g).cuda(), ref.frequencies(d).cuda()
+
+    def chain(wait):
+        y, z = x.clone(), torch.empty_like(x)
+        for i in range(40):
+            dsa.norm_rope(y, None, w, None, f, out=(z, None))
+            if wait:
+                torch.cuda.synchronize()
+            y, _, dw, _ = dsa.norm_rope_bwd(z, None, y, None, w, None, f)
+            if wait:
+                torch.cuda.synchronize()
+        return y, dw
+
+    assert all(torch.equal(a, b) for a, b in zip(chain(False), chain(True)))

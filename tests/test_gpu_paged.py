@@ -516,6 +516,34 @@ def test_decode_step_graph_two_streams():
     assert dsa.device_status() == (0, 0)
 
 
+def test_dependent_steps_back_to_back():
+    """Thirty decode steps, each appending to the cache that the next one reads and feeding it its
+    output, give what they give with the device waited for after every call."""
+    g = torch.Generator().manual_seed(29)
+    page, Hq, Hkv, d, H_I, d_I, k, B, width = 16, 32, 4, 128, 64, 128, 64, 5, 16
+    pool = B * width
+    table = torch.randperm(pool, generator=g).view(B, width).to(torch.int32).cuda()
+    start = [randn(pool, page, Hkv, d, gen=g), randn(pool, page, Hkv, d, gen=g), randn(pool, page, d_I, gen=g)]
+    x0, f = randn(B, Hq, d, gen=g).cuda(), ref.frequencies(128).cuda()
+    w = torch.softmax(torch.randn(B, H_I, generator=g), 1).to(BF16).cuda()
+    lens = [i32([b * 37 + i + 1 for b in range(B)]).cuda() for i in range(30)]
+
+    def run(wait):
+        caches, x, out = [c.cuda() for c in start], x0, []
+        for n in lens:
+            K, qi = x[:, :Hkv].contiguous(), x.repeat(1, 2, 1)
+            got = dsa.decode_step_paged(qi, w, x, K, K, x[:, 0], *caches, table, n, width * page, k, inv_freq=f, idx_inv_freq=f)
+            if wait:
+                torch.cuda.synchronize()
+            x, _ = dsa.norm_rope(got[1], None, torch.ones(d, dtype=BF16, device="cuda"))
+            if wait:
+                torch.cuda.synchronize()
+            out += [got[0], x]
+        return out + caches
+
+    assert all(torch.equal(a, b) for a, b in zip(run(False), run(True)))
+
+
 def test_capture_with_a_second_stream():
     """A captured region in which a call's inputs come from another stream, and the call's outputs go
     back to it, replays as it ran."""
