@@ -26,16 +26,17 @@ def needs_build() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and not needs_build():
-        return LIB
-    nvcc = os.environ.get("NVCC", "nvcc")
-    cmd = [nvcc, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
-           "-cudart", "static", "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills",
-           *extra, "-o", LIB + ".tmp", os.path.join(CSRC, "libdsa.cu")]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
-    os.replace(LIB + ".tmp", LIB)
+    """Builds the library and its Python binding where a source is newer; returns the library's path."""
+    if force or needs_build():
+        nvcc = os.environ.get("NVCC", "nvcc")
+        cmd = [nvcc, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+               "-cudart", "static", "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills",
+               *extra, "-o", LIB + ".tmp", os.path.join(CSRC, "libdsa.cu")]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+        os.replace(LIB + ".tmp", LIB)
+    build_binding(force, verbose)
     return LIB
 
 
@@ -67,4 +68,3 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else [])
-    build_binding(force="--force" in sys.argv, verbose=True)
