@@ -401,7 +401,7 @@ DSA_API int dsa_norm_rope_bwd(const void* Q, int64_t q_stride, const void* K, in
                               size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
- * The paged cache of (7) to (7d).  A pool of num_pages pages of page_size positions each:
+ * The paged cache of (6d) to (6h).  A pool of num_pages pages of page_size positions each:
  *   k_cache, v_cache device bf16 [num_pages, page_size, Hkv, d], k_idx_cache device bf16
  *     [num_pages, page_size, d_I]; *_page_stride: elements from one page to the next (at
  *     least a page, a multiple of 8), so one allocation may hold several caches by turns.
@@ -415,7 +415,7 @@ DSA_API int dsa_norm_rope_bwd(const void* Q, int64_t q_stride, const void* K, in
  * length are not used.
  * Supported: page_size a power of two from 16 to 1024; num_pages * page_size < 2^31.
  *
- * (7) Appends new tokens: K normed and rotated as in (6b), V as it is and k_idx (one head)
+ * (6d) Appends new tokens: K normed and rotated as in (6b), V as it is and k_idx (one head)
  * normed and rotated with its own weight and frequencies, all in one launch.  Token i of
  * sequence b (packed rows, cu_seqlens_q as everywhere) is written at position
  * p = seqlens_k[b] - Lq + i; a token with p < 0, with p past the table or on a page that is
@@ -435,7 +435,7 @@ DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int
                              int batch, int num_pages, int page_size, void* stream);
 
 /* ---------------------------------------------------------------------------------
- * (7a) Indexer scores over the paged cache: (1) with one query row per sequence, which sees
+ * (6e) Indexer scores over the paged cache: (1) with one query row per sequence, which sees
  * its whole cache.  scores device fp32 [batch, ld_scores]: column s < the sequence's length
  * receives position s's score, -inf on a page that is not there; the rest is untouched.
  * (Several query rows of one sequence, as when drafted tokens are checked, are entries of
@@ -450,11 +450,13 @@ DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t 
                             void* stream);
 
 /* ---------------------------------------------------------------------------------
- * (7b) Decode attention over the paged cache: (4) with its positions looked up in the
+ * (6f) Decode attention over the paged cache: (4) with its positions looked up in the
  * table.  Entries of indices outside [0, length) or on a page that is not there are ignored;
  * an empty set gives O = 0 and lse = -inf.  One launch and no workspace.  Two equal entries
  * of a row count twice, as in (3).  Repeats of a call are bit-identical; how a row's slots are
  * split over blocks depends on the batch, so a row's last bits may differ between batches.
+ * (A weight multiplies V as two bf16, the second of either sign: an infinity in a selected V
+ * row gives NaN there.)
  * Supported: the shapes of (4); page_size * Hkv * d < 2^31.
  * ------------------------------------------------------------------------------- */
 DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int64_t k_page_stride,
@@ -465,12 +467,12 @@ DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int
                                          int k, float scale, void* O, float* lse, void* stream);
 
 /* ---------------------------------------------------------------------------------
- * (7c) Whole DSA decode step over the paged cache: (7a), (2), then (7b), on a cache that
+ * (6g) Whole DSA decode step over the paged cache: (6e), (2), then (6f), on a cache that
  * holds the current token already.  indices device int32 [batch, k] receives the sets
  * (positions on pages that are not there come last, where fewer than k others are seen; the
  * attention ignores them).
  *   workspace: dsa_decode_paged_workspace_size(batch, max_seqlen_k) bytes.
- * Supported: the shapes of (7a) and (7b); batch * max_seqlen_k < 2^31.
+ * Supported: the shapes of (6e) and (6f); batch * max_seqlen_k < 2^31.
  * ------------------------------------------------------------------------------- */
 DSA_API size_t dsa_decode_paged_workspace_size(int batch, int max_seqlen_k);
 DSA_API int dsa_decode_paged(const void* q_idx, const void* w, const void* Q, const void* k_cache,
@@ -483,8 +485,8 @@ DSA_API int dsa_decode_paged(const void* q_idx, const void* w, const void* Q, co
                              void* stream);
 
 /* ---------------------------------------------------------------------------------
- * (7d) Whole DSA decode step from the projections of one new token per sequence: Q and
- * q_idx normed and rotated (6b), K, V and k_idx appended (7), in one launch; then (7c).
+ * (6h) Whole DSA decode step from the projections of one new token per sequence: Q and
+ * q_idx normed and rotated (6b), K, V and k_idx appended (6d), in one launch; then (6g).
  * Row b of Q, K, V, q_idx, k_idx and w belongs to sequence b, whose new token sits at
  * position seqlens_k[b] - 1 (rotated at positions[b] where positions is not NULL).
  *   workspace: dsa_decode_step_paged_workspace_size() bytes.
