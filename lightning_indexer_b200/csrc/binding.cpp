@@ -146,11 +146,14 @@ PyObject* pack(const Ts&... ts) {
   return r;
 }
 
+int int32(int64_t v, const char* name) {
+  if (v != (int)v) refuse(std::string(name) + " does not fit in 32 bits");
+  return (int)v;
+}
 int as_int(PyObject* o, const char* name) {
   const long v = PyLong_AsLong(o);
   if (v == -1 && PyErr_Occurred()) throw PyError();
-  if (v != (int)v) refuse(std::string(name) + " does not fit in 32 bits");
-  return (int)v;
+  return int32(v, name);
 }
 float as_float(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
@@ -180,8 +183,8 @@ struct Rope {
   Rope(Call& c, PyObject* o, const char* name) {
     if (o == Py_None) return;
     const Tensor& t = tensor(o, name);
+    rotary = int32(2 * t.numel(), "the rotated width");
     freq = c.arg<double>(o, name, at::kDouble, {t.numel()});
-    rotary = (int)(2 * t.numel());
   }
 };
 
@@ -192,7 +195,7 @@ struct TokenMap {
     positions = c.optional<int32_t>(pos, "positions", at::kInt, {T});
     cu = nullptr;
     if (cu_o != Py_None) {
-      batch = (int)tensor(cu_o, "cu_seqlens_q").numel() - 1;
+      batch = int32(tensor(cu_o, "cu_seqlens_q").numel() - 1, "the number of sequences");
       cu = c.arg<int32_t>(cu_o, "cu_seqlens_q", at::kInt, {batch + 1});
     }
     lens = c.optional<int32_t>(lens_o, "seqlens_k", at::kInt, {batch});
@@ -206,8 +209,8 @@ struct Table {
   Table(Call& c, PyObject* table_o, PyObject* lens_o, int64_t B) {
     const Tensor& t = tensor(table_o, "block_table");
     dims(t, "block_table", 2);
-    width = (int)t.size(1);
-    batch = (int)B;
+    width = int32(t.size(1), "the width of block_table");
+    batch = int32(B, "the number of sequences");
     table = c.arg<int32_t>(table_o, "block_table", at::kInt, {B, t.size(1)});
     lens = c.arg<int32_t>(lens_o, "seqlens_k", at::kInt, {B});
   }
@@ -429,14 +432,14 @@ PyObject* sparse_attn_decode_paged(PyObject* const* a) {
   const KvPool kv(c, a[1], a[2], d);
   const Tensor& idx = tensor(a[3], "indices");
   dims(idx, "indices", 2);
+  const int k = int32(idx.size(1), "the number of slots");
   const int32_t* ip = c.arg<int32_t>(a[3], "indices", at::kInt, {B, idx.size(1)});
   const Table tab(c, a[4], a[5], B);
   const float scale = softmax_scale(a[6], d);
   const DecodeOut o(c, a[7], B, 0, Hq, d, Q, false);
   launch(c, "dsa_sparse_attn_decode_paged", [&](void* st) {
     return dsa_sparse_attn_decode_paged(q, kv.k, kv.ks, kv.v, kv.vs, ip, tab.table, tab.width, tab.lens, tab.batch, (int)kv.pages,
-                                        (int)kv.page, (int)Hq, (int)kv.Hkv, (int)d, (int)idx.size(1), scale, o.O.data_ptr(),
-                                        o.lse_ptr(), st);
+                                        (int)kv.page, (int)Hq, (int)kv.Hkv, (int)d, k, scale, o.O.data_ptr(), o.lse_ptr(), st);
   });
   return pack(o.O, o.lse);
 }

@@ -616,3 +616,17 @@ def test_binding_checks_sizes():
         dsa.index_paged(q, ic, w, table, lens, 48, scores=z(4, 44, t=torch.float32))
     with pytest.raises(dsa.DSAError):
         dsa.decode_paged(q, w, Q, kc, kc, ic, table, lens, 48, 16, workspace=z(64, t=torch.uint8))
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """Sizes that the library takes in 32 bits are refused, not cut (tensors of no rows: no memory)."""
+    z = lambda *s, t=BF16: torch.zeros(*s, dtype=t, device="cuda")  # noqa: E731
+    i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    kc, ic, huge = z(6, 16, 2, 128), z(6, 16, 64), 2 ** 32 + 16
+    bad = [lambda: dsa.sparse_attn_decode_paged(z(0, 8, 128), kc, kc, i(0, huge), i(0, 3), i(0)),
+           lambda: dsa.sparse_attn_decode_paged(z(0, 8, 128), kc, kc, i(0, 16), i(0, huge), i(0)),
+           lambda: dsa.index_paged(z(0, 8, 64), ic, z(0, 8), i(0, huge), i(0), 48),
+           lambda: dsa.index_paged(z(0, 8, 64), ic, z(0, 8), i(0, 3), i(0), huge)]
+    for call in bad:
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
