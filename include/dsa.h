@@ -367,7 +367,9 @@ DSA_API int dsa_decode(const void* q_idx, const void* k_idx, const void* w, cons
  *     is i + seqlens_k[b] - Lq (seqlens_k device int32 [batch]: lengths with these tokens
  *     included), or i where seqlens_k is NULL.  cu_seqlens_q NULL (then batch is 1 and
  *     seqlens_k NULL): one sequence of total_q tokens.
- *   Rows of tokens outside [cu_seqlens_q[0], cu_seqlens_q[batch]) are left untouched.
+ *   Rows of tokens outside [cu_seqlens_q[0], cu_seqlens_q[batch]) are left untouched by
+ *     dsa_norm_rope and written as zeros by dsa_norm_rope_zeroed, which is for outputs that
+ *     hold nothing yet.
  *   Q_out, K_out may be Q, K themselves (same stride); no other overlap is allowed.
  * Supported: d in {32, 64, 128}; rotary_dim a multiple of 16; total_q * heads < 2^31.
  * ------------------------------------------------------------------------------- */
@@ -378,11 +380,18 @@ DSA_API int dsa_norm_rope(const void* Q, int64_t q_stride, const void* K, int64_
                           const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk,
                           int d, void* Q_out, int64_t q_out_stride, void* K_out,
                           int64_t k_out_stride, void* stream);
+DSA_API int dsa_norm_rope_zeroed(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                                 const void* q_weight, const void* k_weight, float eps,
+                                 const double* inv_freq, int rotary_dim, int interleaved,
+                                 const int32_t* positions, const int32_t* cu_seqlens_q,
+                                 const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk,
+                                 int d, void* Q_out, int64_t q_out_stride, void* K_out,
+                                 int64_t k_out_stride, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * (6c) Gradient of (6b).  dQ_out, dK_out are the gradients at its outputs; Q, K its inputs.
- *   dQ, dK device bf16, written for the same rows that (6b) writes; they may be dQ_out,
- *     dK_out themselves (same stride).
+ *   dQ, dK device bf16, written for the same rows that (6b) writes (dsa_norm_rope_bwd_zeroed:
+ *     zeros in the others); they may be dQ_out, dK_out themselves (same stride).
  *   dq_weight, dk_weight device fp32 [d]: the weights' gradients, summed over those tokens
  *     and all heads (overwritten, not added to); each is required exactly where its weight
  *     is not NULL.  The sums are taken in a fixed order: repeats are bit-identical.
@@ -399,6 +408,15 @@ DSA_API int dsa_norm_rope_bwd(const void* Q, int64_t q_stride, const void* K, in
                               int d, void* dQ, int64_t dq_stride, void* dK, int64_t dk_stride,
                               float* dq_weight, float* dk_weight, void* workspace,
                               size_t workspace_bytes, void* stream);
+DSA_API int dsa_norm_rope_bwd_zeroed(const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                                     const void* dQ_out, int64_t dq_out_stride, const void* dK_out,
+                                     int64_t dk_out_stride, const void* q_weight, const void* k_weight,
+                                     float eps, const double* inv_freq, int rotary_dim, int interleaved,
+                                     const int32_t* positions, const int32_t* cu_seqlens_q,
+                                     const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk,
+                                     int d, void* dQ, int64_t dq_stride, void* dK, int64_t dk_stride,
+                                     float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------
  * The paged cache of (6d) to (6h).  A pool of num_pages pages of page_size positions each:

@@ -401,7 +401,8 @@ def norm_rope(Q, K=None, q_weight=None, k_weight=None, inv_freq=None, positions=
     device, radians per position, or None for no rotation.  positions int32 [T]; without them a
     token's position is its index in its sequence of cu_seqlens_q, shifted so that the last one
     sits at seqlens_k - 1 where that is given.  `out` may give (Q', K') to write, the inputs
-    themselves among them; rows outside the sequences are left as they were (see dsa_norm_rope)."""
+    themselves among them; their rows outside the sequences are left as they were, those of new
+    outputs are zeros (see dsa_norm_rope)."""
     return _native().norm_rope(Q, K, q_weight, k_weight, inv_freq, positions, cu_seqlens_q, seqlens_k, interleaved, eps, out)
 
 
@@ -414,7 +415,8 @@ def norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight=None, k_weight=None, inv_freq=N
                   workspace: Optional[torch.Tensor] = None):
     """Gradients (dQ, dK, dq_weight, dk_weight) of norm_rope from those at its outputs: dQ, dK
     bf16, the weights' fp32 [d] (None where there is no weight).  `out` may give (dQ, dK) to
-    write, dQ_out and dK_out themselves among them (see dsa_norm_rope_bwd)."""
+    write, dQ_out and dK_out themselves among them; rows outside the sequences as in norm_rope
+    (see dsa_norm_rope_bwd)."""
     return _native().norm_rope_bwd(Q, K, dQ_out, dK_out, q_weight, k_weight, inv_freq, positions, cu_seqlens_q, seqlens_k,
                                    interleaved, eps, out, workspace)
 

@@ -84,6 +84,8 @@ SIGNATURES = {
                                            c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_f32, c_i64, c_vp, c_vp,
                                            c_vp, c_vp, c_vp, c_vp, c_size, c_vp]),
 }
+for _name in ("dsa_norm_rope", "dsa_norm_rope_bwd"):  # the forms that write zeros outside the sequences
+    SIGNATURES[_name + "_zeroed"] = SIGNATURES[_name]
 
 _lib = None
 

@@ -263,10 +263,12 @@ PyObject* norm_rope(PyObject* const* a) {
   }
   void* qo = c.rows(Qo, "Q out", {T, Hq, d}, &qos);
   if (has_k) ko = c.rows(Ko, "K out", {T, Hk, d}, &kos);
+  // a new tensor holds zeros in the rows of tokens outside the sequences
+  const auto fn = a[10] == Py_None ? dsa_norm_rope_zeroed : dsa_norm_rope;
   if (T > 0)
     launch(c, "dsa_norm_rope", [&](void* st) {
-      return dsa_norm_rope(q, qs, k, ks, gq, gk, eps, rope.freq, rope.rotary, inter, tk.positions, tk.cu, tk.lens,
-                           tk.batch, T, (int)Hq, (int)Hk, (int)d, qo, qos, ko, kos, st);
+      return fn(q, qs, k, ks, gq, gk, eps, rope.freq, rope.rotary, inter, tk.positions, tk.cu, tk.lens, tk.batch, T, (int)Hq,
+                (int)Hk, (int)d, qo, qos, ko, kos, st);
     });
   return pack(Qo, Ko);
 }
@@ -320,11 +322,12 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
   } else if (gq || gk) {
     ws = new_tensor({(int64_t)dsa_norm_rope_bwd_workspace_size(T, (int)Hq, (int)Hk, (int)d)}, at::kByte, Q);
   }
+  const auto fn = a[12] == Py_None ? dsa_norm_rope_bwd_zeroed : dsa_norm_rope_bwd;  // as in norm_rope
   launch(c, "dsa_norm_rope_bwd", [&](void* st) {
-    return dsa_norm_rope_bwd(q, qs, k, ks, dqo, dqos, dko, dkos, gq, gk, eps, rope.freq, rope.rotary, inter, tk.positions,
-                             tk.cu, tk.lens, tk.batch, T, (int)Hq, (int)Hk, (int)d, dq, dqs, dk, dks,
-                             gq ? dgq.data_ptr<float>() : nullptr, gk ? dgk.data_ptr<float>() : nullptr,
-                             ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? (size_t)ws.numel() : 0, st);
+    return fn(q, qs, k, ks, dqo, dqos, dko, dkos, gq, gk, eps, rope.freq, rope.rotary, inter, tk.positions, tk.cu, tk.lens,
+              tk.batch, T, (int)Hq, (int)Hk, (int)d, dq, dqs, dk, dks, gq ? dgq.data_ptr<float>() : nullptr,
+              gk ? dgk.data_ptr<float>() : nullptr, ws.defined() ? ws.data_ptr() : nullptr,
+              ws.defined() ? (size_t)ws.numel() : 0, st);
   });
   return pack(dQ, dK, dgq, dgk);
 }

@@ -72,6 +72,8 @@ constexpr int NR_BWD_WARPS = 8;  // 2 blocks per SM
 struct HeadRowsParams {
   HeadSeg seg[NR_MAX_SEGS];
   int nseg;
+  int zero_outside;  // rows of tokens outside the sequences (offsets given): 0 stay as they are, 1 become zeros
+  int zero_block0;   // forward: the first of the blocks that write those zeros
   float eps;
   TokenMap tk;
 };
@@ -392,6 +394,21 @@ __device__ __forceinline__ int runs_look_up(const TokenMap& tk, const HeadSeg& s
   return t_first;
 }
 
+// Zeros in the rows of tokens outside the sequences, shared out over `warps` warps.
+template <int D>
+__device__ __forceinline__ void zero_outside(const TokenMap& tk, const HeadSeg& s, int w, int warps, int lane) {
+  const int lo = min(max(tk.cu[0], 0), tk.T), hi = min(max(tk.cu[tk.batch], lo), tk.T);
+  const long long n = (long long)(lo + tk.T - hi) * s.heads * (D / 8);
+#pragma unroll 1
+  for (long long i = w * 32LL + lane; i < n; i += warps * 32LL) {
+    const unsigned row = (unsigned)(i / (D / 8));
+    const int t = row_token(s, row);
+    const int in_token = (int)(row - (unsigned)t * (unsigned)s.heads) * D + (int)(i % (D / 8)) * 8;
+    uint16_t* dst = s.y + (long long)(t < lo ? t : t - lo + hi) * s.y_stride + in_token;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 template <int D, bool INTER, int MODE>
 __device__ __forceinline__ void head_rows_fwd(const HeadRowsParams& p, const HeadSeg& s, int warp_in_seg, int lane,
                                               uint8_t* ring, TurnSmem& ts) {
@@ -485,15 +502,26 @@ __device__ __forceinline__ int block_seg(const HeadRowsParams& p) {
 }
 
 // D and INTER (0 or 1) of every segment where they agree, else 0 and -1: the call is then
-// dispatched per segment, at the registers of the largest form.
-template <int D, int INTER>
+// dispatched per segment, at the registers of the largest form.  ZERO: the blocks from zero_block0
+// on write the zeros outside the sequences (a form of its own: in the others the branch alone made
+// the append 3 % slower; in the row loops the zeros cost spills).
+template <int D, int INTER, bool ZERO>
 __global__ void __launch_bounds__(NR_FWD_WARPS * 32, 5) head_rows_fwd_kernel(const __grid_constant__ HeadRowsParams p) {
   pdl_wait();
   pdl_trigger();
   __shared__ __align__(16) uint8_t rings[NR_FWD_WARPS][NR_STAGES * NR_GROUP_BYTES];
   __shared__ TurnSmem ts;
+  const int lane = threadIdx.x % 32;
+  if constexpr (ZERO) {
+    if ((int)blockIdx.x >= p.zero_block0) {
+      const int first = (int)blockIdx.x - p.zero_block0, blocks = (int)gridDim.x - p.zero_block0;
+      for (int i = 0; i < p.nseg; ++i)
+        zero_outside<D>(p.tk, p.seg[i], first * NR_FWD_WARPS + threadIdx.x / 32, blocks * NR_FWD_WARPS, lane);
+      return;
+    }
+  }
   const HeadSeg& s = p.seg[block_seg(p)];
-  const int w = ((int)blockIdx.x - s.block0) * NR_FWD_WARPS + threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int w = ((int)blockIdx.x - s.block0) * NR_FWD_WARPS + threadIdx.x / 32;
   uint8_t* ring = rings[threadIdx.x / 32];
   const int mode = rows_mode(s);
 #define DSA_HEAD_ROWS(DD, II)                                                            \
@@ -542,6 +570,7 @@ __device__ __forceinline__ void head_rows_bwd(const HeadRowsParams& p, const Hea
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue();
+  if (p.zero_outside) zero_outside<D>(p.tk, s, warp_in_seg, s.warps, lane);  // while the first rows fly
   uint4 ga = {}, gb = {};
   if (norm) {
     ga = *reinterpret_cast<const uint4*>(s.g + col.e0);
@@ -734,6 +763,18 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, bool whole, long long tota
   return (int)block;
 }
 
+template <bool ZERO>
+static int head_rows_fwd_kernel_launch(const dsa::HeadRowsParams& p, int d, int inter, int blocks, bool pdl, cudaStream_t stream) {
+  auto kern = d == 128 && inter ? dsa::head_rows_fwd_kernel<128, 1, ZERO>
+              : d == 128        ? dsa::head_rows_fwd_kernel<128, 0, ZERO>
+              : d == 64 && inter ? dsa::head_rows_fwd_kernel<64, 1, ZERO>
+              : d == 64          ? dsa::head_rows_fwd_kernel<64, 0, ZERO>
+              : d == 32 && inter ? dsa::head_rows_fwd_kernel<32, 1, ZERO>
+              : d == 32          ? dsa::head_rows_fwd_kernel<32, 0, ZERO>
+                                 : dsa::head_rows_fwd_kernel<0, -1, false>;
+  return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_FWD_WARPS * 32), 0, stream, p);
+}
+
 // Forward: a warp for every run.  Blocks that come and go balance rows of different cost: at
 // 32768 tokens of 32 + 4 heads 102 us, against 106 to 142 us in one wave of warps that walk
 // many runs, by how the tensors' costs are weighted; an append of as many, 34 against 48 to 58.
@@ -745,19 +786,17 @@ int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) 
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
   const long long wave = 20LL * sm_count();  // resident warps
   const int run = (int)std::max<long long>(1, std::min<long long>(8, groups / wave));
-  const int blocks = plan_segs(p, run, 2 * groups > 3 * wave, 0, dsa::NR_FWD_WARPS);
+  int blocks = plan_segs(p, run, 2 * groups > 3 * wave, 0, dsa::NR_FWD_WARPS);
   int d = p.seg[0].D, inter = p.seg[0].interleaved;
   for (int i = 1; i < p.nseg; ++i) {
     if (p.seg[i].D != d || p.seg[i].interleaved != inter) d = 0;
   }
-  auto kern = d == 128 && inter ? dsa::head_rows_fwd_kernel<128, 1>
-              : d == 128        ? dsa::head_rows_fwd_kernel<128, 0>
-              : d == 64 && inter ? dsa::head_rows_fwd_kernel<64, 1>
-              : d == 64          ? dsa::head_rows_fwd_kernel<64, 0>
-              : d == 32 && inter ? dsa::head_rows_fwd_kernel<32, 1>
-              : d == 32          ? dsa::head_rows_fwd_kernel<32, 0>
-                                 : dsa::head_rows_fwd_kernel<0, -1>;
-  return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_FWD_WARPS * 32), 0, stream, p);
+  if (p.zero_outside) {  // (Q and K of one call agree)
+    p.zero_block0 = blocks;
+    blocks += std::min(blocks, sm_count());
+    return head_rows_fwd_kernel_launch<true>(p, d, inter, blocks, pdl, stream);
+  }
+  return head_rows_fwd_kernel_launch<false>(p, d, inter, blocks, pdl, stream);
 }
 
 // Blocks of the backward: one wave, two blocks on every SM, since each block adds a share to

@@ -64,6 +64,74 @@ static dsa::TokenMap token_map(const int32_t* positions, const int32_t* cu, cons
   return tk;
 }
 
+// (6b) and (6c).  zero_outside: rows of tokens outside the sequences are written as zeros.
+static int norm_rope_call(const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* q_weight,
+                          const void* k_weight, float eps, const double* inv_freq, int rotary_dim, int interleaved,
+                          const int32_t* positions, const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int batch,
+                          int64_t total_q, int Hq, int Hk, int d, void* Q_out, int64_t q_out_stride, void* K_out,
+                          int64_t k_out_stride, bool zero_outside, void* stream) {
+  const int st = norm_rope_args_status(Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rotary_dim,
+                                       cu_seqlens_q, seqlens_k, batch, total_q, Hq, Hk, d);
+  if (st == DSA_ERR_INVALID_ARG) return st;
+  if (!rows_ok(Q_out, q_out_stride, Hq, d) || (K && !rows_ok(K_out, k_out_stride, Hk, d))) return DSA_ERR_INVALID_ARG;
+  if (st != DSA_OK) return st;
+  if (total_q == 0) return DSA_OK;
+  dsa::HeadRowsParams p{};
+  p.eps = eps;
+  p.zero_outside = zero_outside && cu_seqlens_q;
+  p.tk = token_map(positions, cu_seqlens_q, seqlens_k, batch, total_q);
+  // K's few heads per token cost more per row: they go first
+  if (K) p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, K_out, k_out_stride);
+  p.seg[p.nseg++] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, Q_out, q_out_stride);
+  return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
+}
+
+static int norm_rope_bwd_call(const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* dQ_out,
+                              int64_t dq_out_stride, const void* dK_out, int64_t dk_out_stride, const void* q_weight,
+                              const void* k_weight, float eps, const double* inv_freq, int rotary_dim,
+                              int interleaved, const int32_t* positions, const int32_t* cu_seqlens_q,
+                              const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk, int d, void* dQ,
+                              int64_t dq_stride, void* dK, int64_t dk_stride, float* dq_weight, float* dk_weight,
+                              void* workspace, size_t workspace_bytes, bool zero_outside, void* stream) {
+  const int st = norm_rope_args_status(Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rotary_dim,
+                                       cu_seqlens_q, seqlens_k, batch, total_q, Hq, Hk, d);
+  if (st == DSA_ERR_INVALID_ARG) return st;
+  if (!rows_ok(dQ_out, dq_out_stride, Hq, d) || (K && !rows_ok(dK_out, dk_out_stride, Hk, d)) ||
+      !rows_ok(dQ, dq_stride, Hq, d) || (K && !rows_ok(dK, dk_stride, Hk, d)))
+    return DSA_ERR_INVALID_ARG;
+  if ((q_weight && !dq_weight) || (K && k_weight && !dk_weight)) return DSA_ERR_INVALID_ARG;
+  if (st != DSA_OK) return st;
+  const bool norms = q_weight || (K && k_weight);
+  if (norms && total_q > 0 &&
+      (!workspace || !aligned16(workspace) ||
+       workspace_bytes < norm_rope_bwd_ws_bytes(total_q, Hq, K ? Hk : 0, d)))
+    return DSA_ERR_WORKSPACE;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (total_q == 0) {  // the sums over no rows
+    if (q_weight)
+      if (const cudaError_t e = cudaMemsetAsync(dq_weight, 0, (size_t)d * 4, s); e != cudaSuccess) return cuda_fail(e);
+    if (K && k_weight)
+      if (const cudaError_t e = cudaMemsetAsync(dk_weight, 0, (size_t)d * 4, s); e != cudaSuccess) return cuda_fail(e);
+    return DSA_OK;
+  }
+  dsa::HeadRowsParams p{};
+  p.eps = eps;
+  p.zero_outside = zero_outside && cu_seqlens_q;
+  p.tk = token_map(positions, cu_seqlens_q, seqlens_k, batch, total_q);
+  float* dg[2] = {dq_weight, dk_weight};
+  p.seg[0] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, dQ, dq_stride);
+  p.seg[0].dy = static_cast<const uint16_t*>(dQ_out);
+  p.seg[0].dy_stride = (int)dq_out_stride;
+  p.nseg = 1;
+  if (K) {
+    p.seg[1] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, dK, dk_stride);
+    p.seg[1].dy = static_cast<const uint16_t*>(dK_out);
+    p.seg[1].dy_stride = (int)dk_out_stride;
+    p.nseg = 2;
+  }
+  return head_rows_bwd_launch(p, static_cast<float*>(workspace), dg, s);
+}
+
 // Checks of a paged cache's description, in the documented order (a cache may be absent).
 static int paged_args_status(const int32_t* table, int max_pages, const int32_t* lens, int batch, int num_pages,
                              int page_size) {
@@ -275,19 +343,19 @@ DSA_API int dsa_norm_rope(const void* Q, int64_t q_stride, const void* K, int64_
                           const int32_t* positions, const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int batch,
                           int64_t total_q, int Hq, int Hk, int d, void* Q_out, int64_t q_out_stride, void* K_out,
                           int64_t k_out_stride, void* stream) {
-  const int st = norm_rope_args_status(Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rotary_dim,
-                                       cu_seqlens_q, seqlens_k, batch, total_q, Hq, Hk, d);
-  if (st == DSA_ERR_INVALID_ARG) return st;
-  if (!rows_ok(Q_out, q_out_stride, Hq, d) || (K && !rows_ok(K_out, k_out_stride, Hk, d))) return DSA_ERR_INVALID_ARG;
-  if (st != DSA_OK) return st;
-  if (total_q == 0) return DSA_OK;
-  dsa::HeadRowsParams p{};
-  p.eps = eps;
-  p.tk = token_map(positions, cu_seqlens_q, seqlens_k, batch, total_q);
-  // K's few heads per token cost more per row: they go first
-  if (K) p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, K_out, k_out_stride);
-  p.seg[p.nseg++] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, Q_out, q_out_stride);
-  return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
+  return norm_rope_call(Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rotary_dim, interleaved, positions,
+                        cu_seqlens_q, seqlens_k, batch, total_q, Hq, Hk, d, Q_out, q_out_stride, K_out, k_out_stride, false,
+                        stream);
+}
+
+DSA_API int dsa_norm_rope_zeroed(const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* q_weight,
+                                 const void* k_weight, float eps, const double* inv_freq, int rotary_dim, int interleaved,
+                                 const int32_t* positions, const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int batch,
+                                 int64_t total_q, int Hq, int Hk, int d, void* Q_out, int64_t q_out_stride, void* K_out,
+                                 int64_t k_out_stride, void* stream) {
+  return norm_rope_call(Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rotary_dim, interleaved, positions,
+                        cu_seqlens_q, seqlens_k, batch, total_q, Hq, Hk, d, Q_out, q_out_stride, K_out, k_out_stride, true,
+                        stream);
 }
 
 DSA_API size_t dsa_norm_rope_bwd_workspace_size(int64_t total_q, int Hq, int Hk, int d) {
@@ -302,42 +370,23 @@ DSA_API int dsa_norm_rope_bwd(const void* Q, int64_t q_stride, const void* K, in
                               const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk, int d, void* dQ,
                               int64_t dq_stride, void* dK, int64_t dk_stride, float* dq_weight, float* dk_weight,
                               void* workspace, size_t workspace_bytes, void* stream) {
-  const int st = norm_rope_args_status(Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rotary_dim,
-                                       cu_seqlens_q, seqlens_k, batch, total_q, Hq, Hk, d);
-  if (st == DSA_ERR_INVALID_ARG) return st;
-  if (!rows_ok(dQ_out, dq_out_stride, Hq, d) || (K && !rows_ok(dK_out, dk_out_stride, Hk, d)) ||
-      !rows_ok(dQ, dq_stride, Hq, d) || (K && !rows_ok(dK, dk_stride, Hk, d)))
-    return DSA_ERR_INVALID_ARG;
-  if ((q_weight && !dq_weight) || (K && k_weight && !dk_weight)) return DSA_ERR_INVALID_ARG;
-  if (st != DSA_OK) return st;
-  const bool norms = q_weight || (K && k_weight);
-  if (norms && total_q > 0 &&
-      (!workspace || !aligned16(workspace) ||
-       workspace_bytes < dsa_norm_rope_bwd_workspace_size(total_q, Hq, K ? Hk : 0, d)))
-    return DSA_ERR_WORKSPACE;
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (total_q == 0) {  // the sums over no rows
-    if (q_weight)
-      if (const cudaError_t e = cudaMemsetAsync(dq_weight, 0, (size_t)d * 4, s); e != cudaSuccess) return cuda_fail(e);
-    if (K && k_weight)
-      if (const cudaError_t e = cudaMemsetAsync(dk_weight, 0, (size_t)d * 4, s); e != cudaSuccess) return cuda_fail(e);
-    return DSA_OK;
-  }
-  dsa::HeadRowsParams p{};
-  p.eps = eps;
-  p.tk = token_map(positions, cu_seqlens_q, seqlens_k, batch, total_q);
-  float* dg[2] = {dq_weight, dk_weight};
-  p.seg[0] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, dQ, dq_stride);
-  p.seg[0].dy = static_cast<const uint16_t*>(dQ_out);
-  p.seg[0].dy_stride = (int)dq_out_stride;
-  p.nseg = 1;
-  if (K) {
-    p.seg[1] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, dK, dk_stride);
-    p.seg[1].dy = static_cast<const uint16_t*>(dK_out);
-    p.seg[1].dy_stride = (int)dk_out_stride;
-    p.nseg = 2;
-  }
-  return head_rows_bwd_launch(p, static_cast<float*>(workspace), dg, s);
+  return norm_rope_bwd_call(Q, q_stride, K, k_stride, dQ_out, dq_out_stride, dK_out, dk_out_stride, q_weight, k_weight,
+                            eps, inv_freq, rotary_dim, interleaved, positions, cu_seqlens_q, seqlens_k, batch, total_q,
+                            Hq, Hk, d, dQ, dq_stride, dK, dk_stride, dq_weight, dk_weight, workspace, workspace_bytes,
+                            false, stream);
+}
+
+DSA_API int dsa_norm_rope_bwd_zeroed(const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* dQ_out,
+                                     int64_t dq_out_stride, const void* dK_out, int64_t dk_out_stride, const void* q_weight,
+                                     const void* k_weight, float eps, const double* inv_freq, int rotary_dim,
+                                     int interleaved, const int32_t* positions, const int32_t* cu_seqlens_q,
+                                     const int32_t* seqlens_k, int batch, int64_t total_q, int Hq, int Hk, int d, void* dQ,
+                                     int64_t dq_stride, void* dK, int64_t dk_stride, float* dq_weight, float* dk_weight,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  return norm_rope_bwd_call(Q, q_stride, K, k_stride, dQ_out, dq_out_stride, dK_out, dk_out_stride, q_weight, k_weight,
+                            eps, inv_freq, rotary_dim, interleaved, positions, cu_seqlens_q, seqlens_k, batch, total_q,
+                            Hq, Hk, d, dQ, dq_stride, dK, dk_stride, dq_weight, dk_weight, workspace, workspace_bytes,
+                            true, stream);
 }
 
 DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int64_t v_stride, const void* k_idx,

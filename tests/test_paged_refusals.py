@@ -50,6 +50,13 @@ def test_norm_rope_bwd_refusals():
     refused("dsa_norm_rope_bwd", base, order, cases)
 
 
+@pytest.mark.parametrize("name", ["dsa_norm_rope_zeroed", "dsa_norm_rope_bwd_zeroed"])
+def test_zeroed_forms_refuse_the_same(name, monkeypatch):
+    lib, plain = _lib.load(), name.removesuffix("_zeroed")
+    monkeypatch.setattr(lib, plain, getattr(lib, name))
+    test_norm_rope_refusals() if plain == "dsa_norm_rope" else test_norm_rope_bwd_refusals()
+
+
 POOL = dict(table=FAKE, width=8, lens=FAKE, batch=2, pages=16, page=16)
 POOL_CASES = [(dict(table=None), BAD_ARG), (dict(lens=None), BAD_ARG), (dict(width=0), BAD_ARG), (dict(batch=0), BAD_ARG),
               (dict(pages=0), BAD_ARG), (dict(page=0), BAD_ARG), (dict(page=8), UNSUPPORTED), (dict(page=48), UNSUPPORTED),
