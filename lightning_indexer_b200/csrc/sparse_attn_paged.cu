@@ -32,6 +32,17 @@ __device__ __forceinline__ void cp_async_16_all(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// An attention weight p >= 0 in two parts.  The heads of two weights as bf16 pairs, cut, not rounded:
+// the rest is then never negative.
+__device__ __forceinline__ uint32_t weight_heads(float p0, float p1) {
+  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+}
+// What the head leaves of p, at least the smallest bf16 (2^-133, nothing next to any weight) where
+// p > 0: a rest of 0 would turn an infinity in V into NaN.
+__device__ __forceinline__ float weight_rest(float p) {
+  return fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xFFFF0000u), fminf(p, 9.18354962e-41f));
+}
+
 struct SAPagedParams {
   const uint16_t* Q;  // [rows, Hq, D]
   const uint16_t* K;  // [pages, P, Hkv, D], page strides below (elements)
@@ -236,11 +247,13 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
       const float p10 = exp2f(x10 - mu0), p11 = exp2f(x11 - mu1);
       l0 += p00 + p10;
       l1 += p01 + p11;
-      // ---- O^T += V^T . P^T, each weight as two bf16 (what the first rounds off is the second, so
-      // 2^-16 of a weight is lost, not 2^-8); V's fragments serve both products
-      const uint32_t hi0 = pack_bf16x2(p00, p01), hi1 = pack_bf16x2(p10, p11);
-      const uint32_t lo0 = pack_bf16x2(p00 - __uint_as_float(hi0 << 16), p01 - __uint_as_float(hi0 & 0xFFFF0000u));
-      const uint32_t lo1 = pack_bf16x2(p10 - __uint_as_float(hi1 << 16), p11 - __uint_as_float(hi1 & 0xFFFF0000u));
+      // ---- O^T += V^T . P^T, each weight as two bf16: its leading 8 bits, cut, and what that cuts
+      // off, rounded, so 2^-16 of a weight is lost, not 2^-8.  Both are positive where the weight
+      // is (see weight_rest), so that an infinity in V meets no other sign and no zero.  V's
+      // fragments serve both products.
+      const uint32_t hi0 = weight_heads(p00, p01), hi1 = weight_heads(p10, p11);
+      const uint32_t lo0 = pack_bf16x2(weight_rest(p00), weight_rest(p01));
+      const uint32_t lo1 = pack_bf16x2(weight_rest(p10), weight_rest(p11));
       const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
       const uint32_t c0 = movmatrix_trans(lo0), c1 = movmatrix_trans(lo1);
 #pragma unroll

@@ -1,0 +1,88 @@
+"""Infinities and NaN among what the paged attention and the paged indexer read: they reach the
+results as the formulas carry them, and nothing else."""
+import math
+
+import pytest
+import torch
+
+import lightning_indexer_b200 as dsa
+import paged_testutil as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+INF, NAN = float("inf"), float("nan")
+
+
+def pages(Hq, Hkv, d, page, n, k, seed):
+    """One sequence of n positions, k of them selected (all where k >= n), on shuffled pages."""
+    g = torch.Generator().manual_seed(seed)
+    width = (n + page - 1) // page
+    table = torch.randperm(width, generator=g)[None].to(torch.int32)
+    Q, kc, vc = (torch.randn(*s, generator=g).to(BF16) for s in ((1, Hq, d), (width, page, Hkv, d), (width, page, Hkv, d)))
+    sel = torch.randperm(n, generator=g)[:k].sort().values
+    idx = torch.full((1, k), -1, dtype=torch.int32)
+    idx[0, :len(sel)] = sel.to(torch.int32)
+    return Q, kc, vc, idx, table, sel
+
+
+def attend(Q, kc, vc, idx, table, n, **kw):
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    O, lse = dsa.sparse_attn_decode_paged(Q.cuda(), kc.cuda(), vc.cuda(), idx.cuda(), table.cuda(), lens, **kw)
+    return O[0].cpu(), lse[0].cpu()
+
+
+def plain(Q, K, V, scale):
+    """O [Hq, d] and lse [Hq] of one row in 64 bits, and the bound on a finite O (the paged attention's:
+    weights to 2^-16, logits and exponentials 2e-4, the output's own rounding)."""
+    G = Q.shape[0] // K.shape[1]
+    K, V = (x.double().repeat_interleave(G, 1).transpose(0, 1) for x in (K, V))
+    x = (K @ Q.double()[:, :, None])[:, :, 0] * scale
+    m = x.amax(1, keepdim=True)
+    p = torch.exp(x - m)
+    total = p.sum(1, keepdim=True)
+    O = ((p / total)[:, :, None] * V).sum(1)
+    spread = ((p / total)[:, :, None] * (V - O[:, None]).abs()).sum(1)
+    return O, (m + torch.log(total))[:, 0], (2.0 ** -16 + 2e-4) * spread + 2.0 ** -8 * O.abs() * 1.01 + 1e-6
+
+
+def same_where_not_finite(got, want):
+    """Infinities of the same sign and NaN in the same places; returns where both are finite."""
+    got = got.double()
+    assert torch.equal(got.isnan(), want.isnan())
+    inf = want.isinf()
+    assert torch.equal(got.isinf(), inf) and torch.equal(got[inf], want[inf])
+    return want.isfinite()
+
+
+SHAPES = [(32, 4, 128), (8, 2, 64)]
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
+@pytest.mark.parametrize("n,k", [(1, 16), (20, 32), (700, 512), (3000, 2048)])
+def test_infinity_in_a_selected_value(Hq, Hkv, d, n, k):
+    """A weight times an infinity is that infinity; opposite ones, and NaN, give NaN; the other dims and
+    KV heads stay finite."""
+    page = 16
+    Q, kc, vc, idx, table, sel = pages(Hq, Hkv, d, page, n, k, n + d)
+
+    def put(s, head, dim, value):
+        s = int(s)
+        vc[int(table[0, s // page]), s % page, head, dim] = value
+
+    put(sel[-1], 0, 3, INF)
+    put(sel[0], 0, 4, -INF)
+    put(sel[len(sel) // 2], 1, d - 1, -INF)
+    if n > 1:
+        put(sel[1], 1, 0, INF)
+        put(sel[-2], 1, 0, INF)
+        put(sel[1], 0, 7, INF)
+        put(sel[-1], 0, 7, -INF)
+        put(sel[2], 1, 9, NAN)
+    O, lse = attend(Q, kc, vc, idx, table, n)
+    at = table[0].long()[sel // page], sel % page
+    want, wlse, bound = plain(Q[0], kc[at], vc[at], d ** -0.5)
+    assert bool(want.isinf().any())
+    fin = same_where_not_finite(O, want)
+    assert bool(((O.double() - want).abs() <= bound)[fin].all())
+    assert float((lse.double() - wlse).abs().max()) <= 5e-4
