@@ -475,6 +475,7 @@ DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t 
  * split over blocks depends on the batch, so a row's last bits may differ between batches.
  * An infinity in a selected V row gives that infinity, as the formula has it, and NaN gives
  * NaN (a weight below 2^-133 of the row's largest counts as 0, and 0 times an infinity is NaN).
+ * A NaN logit, or one that is +inf, makes the head's O and lse NaN.
  * Supported: the shapes of (4); page_size * Hkv * d < 2^31.
  * ------------------------------------------------------------------------------- */
 DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int64_t k_page_stride,

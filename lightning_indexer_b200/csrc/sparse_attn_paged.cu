@@ -324,11 +324,12 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
     }
   };
   auto finish = [&](int v, float M, float L, const float4& o) {
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const bool none = L == 0.f;  // a NaN sum is not an empty set
+    const float inv = none ? 0.f : 1.f / L;
     const int h = v / (D / 4);
     *reinterpret_cast<uint2*>(p.O + head0 * D + v * 4) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (p.lse && v % (D / 4) == 0) p.lse[head0 + h] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+    if (p.lse && v % (D / 4) == 0) p.lse[head0 + h] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
   };
   if (splits > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int v = threadIdx.x; v < pieces; v += WARPS * 32) {

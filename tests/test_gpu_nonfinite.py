@@ -86,3 +86,27 @@ def test_infinity_in_a_selected_value(Hq, Hkv, d, n, k):
     fin = same_where_not_finite(O, want)
     assert bool(((O.double() - want).abs() <= bound)[fin].all())
     assert float((lse.double() - wlse).abs().max()) <= 5e-4
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", SHAPES)
+@pytest.mark.parametrize("n,k", [(1, 16), (40, 48), (3000, 2048)])
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_nan_reaches_lse(Hq, Hkv, d, n, k, value):
+    """A NaN or an infinite logit makes the row's lse NaN: -inf says that nothing was selected."""
+    page = 32
+    Q, kc, vc, idx, table, sel = pages(Hq, Hkv, d, page, n, k, n + d + 1)
+    Q = Q.abs() + 0.5  # an infinite key gives an infinite logit
+    s, G = int(sel[len(sel) // 2]), Hq // Hkv
+    kc[int(table[0, s // page]), s % page, 1] = value
+    O, lse = attend(Q, kc, vc, idx, table, n)
+    hit = torch.arange(Hq) // G == 1
+    assert bool(lse[hit].isnan().all()) and bool(O[hit].isnan().all())
+    at = table[0].long()[sel // page], sel % page
+    want, wlse, bound = plain(Q[0], kc[at], vc[at], d ** -0.5)
+    assert bool(((O.double() - want).abs() <= bound)[~hit].all())
+    # logits of 128 products up to 60 in size: fp32 sums are off by 128 * 2^-24 * 60 = 4.6e-4
+    assert float((lse.double() - wlse).abs()[~hit].max()) <= 1e-3
+    # the masked kind does not count: the same value in a position that is not selected
+    empty = torch.full_like(idx, -1)
+    O, lse = attend(Q, kc, vc, empty, table, n)
+    assert bool((O == 0).all()) and bool((lse == -math.inf).all())
