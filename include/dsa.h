@@ -458,6 +458,8 @@ DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int
  * receives position s's score, -inf on a page that is not there; the rest is untouched.
  * (Several query rows of one sequence, as when drafted tokens are checked, are entries of
  * their own with the same table row and growing lengths.)
+ * A NaN among the products of a position makes its score NaN ((2) ranks NaN first), where (1)
+ * takes it as 0; what a page holds behind a sequence's length does not matter.
  * ld_scores >= max_seqlen_k and a multiple of 4.
  * Supported: the (H_I, d_I) of (1); batch * H_I < 2^31; max_seqlen_k < 2^31 - 1024.
  * ------------------------------------------------------------------------------- */

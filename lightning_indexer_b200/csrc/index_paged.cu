@@ -25,6 +25,13 @@
 
 namespace dsa {
 
+// max(0, x), and NaN for NaN: a broken key or query must not score like an unrelated one.
+__device__ __forceinline__ float relu(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 struct IndexPagedParams {
   const uint16_t* w;  // [batch, H_I]
   const int* lens;    // [batch]
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(224, 1)
           tmem_ld_x16_sync(tbase + h0, v);
 #pragma unroll
           for (int q = 0; q < 16; ++q)
-            if (h0 + q < H_I) acc = fmaf(wr[h0 + q < H_I ? h0 + q : 0], fmaxf(v[q], 0.f), acc);
+            if (h0 + q < H_I) acc = fmaf(wr[h0 + q < H_I ? h0 + q : 0], relu(v[q]), acc);
         }
         tc_fence_before();
         __syncwarp();

@@ -110,3 +110,51 @@ def test_nan_reaches_lse(Hq, Hkv, d, n, k, value):
     empty = torch.full_like(idx, -1)
     O, lse = attend(Q, kc, vc, empty, table, n)
     assert bool((O == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("H_I,d_I", [(64, 128), (32, 128), (16, 128), (8, 64), (4, 32)])
+@pytest.mark.parametrize("page", [16, 256])
+def test_indexer_scores_carry_nan_and_infinity(H_I, d_I, page):
+    """A NaN in a key makes its score NaN and no other; one in the query, the whole row; an infinite
+    product counts as it is where it is positive and as 0 where it is negative."""
+    g = torch.Generator().manual_seed(H_I + page)
+    lens = [300, 131, 1, 0, 77]
+    pool = sum((n + page - 1) // page for n in lens) + 1
+    table = ref.page_table(lens, page, pool, g)
+    q = (torch.randint(0, 2, (5, H_I, d_I), generator=g) * 2 - 1).to(BF16)  # +-1: no product of 0 and infinity
+    cache = torch.randint(-8, 9, (pool, page, d_I), generator=g).to(BF16)
+    w = (0.5 ** torch.randint(1, 4, (5, H_I), generator=g)).to(BF16)
+
+    def put(b, s, dim, value):
+        cache[int(table[b, s // page]), s % page, dim] = value
+
+    put(0, 0, 1, NAN), put(0, 127, 0, -NAN), put(0, 299, d_I - 1, NAN), put(1, 130, 5, NAN)
+    put(0, 128, 2, INF), put(1, 7, 3, -INF), put(2, 0, 4, INF)
+    q[4, 1, 2] = NAN
+    unused = torch.ones(pool, page, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        s = torch.arange(n)
+        unused[table[b].long()[s // page], s % page] = False
+    cache[unused] = NAN  # behind the lengths and on pages of no sequence
+    dev = [x.cuda() for x in (q, cache, w, table, torch.tensor(lens, dtype=torch.int32))]
+    scores = dsa.index_paged(*dev, 300).cpu()
+    for b, n in enumerate(lens):
+        assert bool((scores[b, n:] == -INF).all())
+        if n == 0:
+            continue
+        dots = torch.einsum("hd,sd->hs", q[b].double(), ref.f64(ref.cached(cache, table, b, n, page)))
+        want = (w[b].double()[:, None] * torch.where(dots < 0, 0.0, dots)).sum(0)  # a NaN product stays
+        fin = same_where_not_finite(scores[b, :n], want)
+        assert torch.equal(scores[b, :n].double()[fin], want[fin]), b
+    assert bool(scores[4, :77].isnan().all()) and int(scores[0, :300].isnan().sum()) == 3
+    # through the decode: the sets of NaN scores are sets all the same, NaN first
+    k = 16
+    kc = torch.randn(pool, page, 2, 64, generator=g).to(BF16).cuda()
+    Q = torch.randn(5, 8, 64, generator=g).to(BF16).cuda()
+    idx, O, lse = dsa.decode_paged(dev[0], dev[2], Q, kc, kc, dev[1], dev[3], dev[4], 300, k)
+    idx = idx.cpu()
+    for b, n in enumerate(lens):
+        sel = idx[b][idx[b] >= 0]
+        assert len(sel) == min(k, n) == len(sel.unique()) and bool((sel < n).all())
+    assert {0, 127, 299} <= set(idx[0].tolist()) and 130 in idx[1].tolist()
+    assert bool(O.isfinite().all())
