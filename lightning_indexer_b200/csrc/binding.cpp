@@ -315,7 +315,8 @@ PyObject* norm_rope_bwd(PyObject* const* a) {
     return pack(dQ, dK, dgq, dgk);
   }
   if (gq) dgq = new_tensor({d}, at::kFloat, Q);
-  if (gk) dgk = new_tensor({d}, at::kFloat, Q);
+  // (K of no heads has a null pointer and takes no part in the call)
+  if (gk) dgk = Hk > 0 ? new_tensor({d}, at::kFloat, Q) : at::zeros({d}, Q.options().dtype(at::kFloat));
   if (a[13] != Py_None) {
     ws = tensor(a[13], "workspace");
     c.dense(ws, "workspace", at::kByte, {ws.numel()});

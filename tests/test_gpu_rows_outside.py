@@ -73,3 +73,16 @@ def test_rows_outside_the_sequences(T, Hq, Hk, d, rotary, inter, norm, offsets):
     torch.cuda.synchronize()
     for x in (y, dx):
         assert bool((x[:lo] == 0).all()) and bool((x[hi:] == 0).all()) and not bool(x.isnan().any())
+
+
+def test_no_key_heads():
+    """K of no heads: its outputs are empty and its weight's gradient, a sum over no rows, is zero."""
+    Q = torch.ones(5, 4, 64, dtype=BF16, device="cuda")
+    K, w = Q[:, :0], torch.ones(64, dtype=BF16, device="cuda")
+    held = [torch.full((64,), float("nan"), device="cuda") for _ in range(200)]
+    torch.cuda.synchronize()
+    del held
+    dQ, dK, dgq, dgk = dsa.norm_rope_bwd(Q, K, Q, K, w, w)
+    want = dsa.norm_rope_bwd(Q, None, Q, None, w, None)
+    assert dK.shape == K.shape and torch.equal(dQ, want[0]) and torch.equal(dgq, want[2])
+    assert bool((dgk == 0).all())
