@@ -68,6 +68,7 @@ struct TokenMap {
 constexpr int NR_MAX_SEGS = 5;
 constexpr int NR_FWD_WARPS = 4;  // warps of a block; 5 blocks per SM at 102 registers (8 x 3 spills, 8 x 2 waits)
 constexpr int NR_BWD_WARPS = 8;  // 2 blocks per SM
+constexpr int NR_BWD_BLOCKS = 2 * 148;
 
 struct HeadRowsParams {
   HeadSeg seg[NR_MAX_SEGS];
@@ -799,11 +800,12 @@ int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) 
   return head_rows_fwd_kernel_launch<false>(p, d, inter, blocks, pdl, stream);
 }
 
-// Blocks of the backward: one wave, two blocks on every SM, since each block adds a share to
-// the weights' gradients.  They set the order of those sums and the size of the workspace, so
-// they follow from the sizes alone.
+// Blocks of the backward: one wave, two blocks on each of a B200's SMs, since each block adds a
+// share to the weights' gradients.  They set the order of those sums and the size of the
+// workspace, so they follow from the sizes alone and not from the device that is current when
+// either is asked for.
 static int bwd_plan(dsa::HeadRowsParams& p) {
-  const long long blocks = 2LL * sm_count();
+  const long long blocks = dsa::NR_BWD_BLOCKS;
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
   const long long warps = blocks * dsa::NR_BWD_WARPS;

@@ -50,6 +50,14 @@ def test_norm_rope_bwd_refusals():
     refused("dsa_norm_rope_bwd", base, order, cases)
 
 
+def test_norm_rope_bwd_workspace_follows_from_the_sizes():
+    """A share of d sums for each block, at most 296 blocks, whatever device is current (or none)."""
+    size = _lib.load().dsa_norm_rope_bwd_workspace_size
+    for T, Hq, Hk, d in ((65536, 32, 4, 128), (1 << 20, 64, 1, 64), (40000, 32, 0, 128)):
+        assert size(T, Hq, Hk, d) == 296 * d * 4
+    assert 0 < size(1, 1, 0, 32) <= size(1000, 8, 2, 64) <= 296 * 64 * 4
+
+
 @pytest.mark.parametrize("name", ["dsa_norm_rope_zeroed", "dsa_norm_rope_bwd_zeroed"])
 def test_zeroed_forms_refuse_the_same(name, monkeypatch):
     lib, plain = _lib.load(), name.removesuffix("_zeroed")
