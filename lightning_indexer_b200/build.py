@@ -40,9 +40,18 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
+def _binding_stamp() -> str:
+    """What the binding holds of the interpreter and the torch that it was built against."""
+    import torch
+    return f"dsa-binding python {sysconfig.get_python_version()} torch {torch.__version__}"
+
+
 def needs_binding() -> bool:
     hdr = os.path.join(os.path.dirname(HERE), "include", "dsa.h")
-    return not os.path.exists(BINDING) or any(os.path.getmtime(f) > os.path.getmtime(BINDING) for f in (BINDING_SRC, hdr))
+    if not os.path.exists(BINDING) or any(os.path.getmtime(f) > os.path.getmtime(BINDING) for f in (BINDING_SRC, hdr)):
+        return True
+    with open(BINDING, "rb") as f:  # torch's C++ interface changes with its version
+        return _binding_stamp().encode() + b"\0" not in f.read()
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
@@ -54,9 +63,9 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     tdir = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(tdir, "include"),
-           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"), BINDING_SRC, "-o", BINDING + ".tmp",
-           "-L" + os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-L" + HERE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DDSA_BINDING_STAMP="{_binding_stamp()}"',
+           "-I" + os.path.join(tdir, "include"), "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+           BINDING_SRC, "-o", BINDING + ".tmp", "-L" + os.path.join(tdir, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-L" + HERE,
            "-l:libdsa_b200.so", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)

@@ -560,4 +560,9 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module_def); }
+PyMODINIT_FUNC PyInit__binding() {
+  PyObject* m = PyModule_Create(&module_def);
+  // read by the build, which makes the module anew for another torch or Python
+  if (m && PyModule_AddStringConstant(m, "built_for", DSA_BINDING_STAMP) < 0) Py_CLEAR(m);
+  return m;
+}
