@@ -358,7 +358,7 @@ namespace dsa_host {
 
 template <int H_I, int D_I>
 static int index_paged_launch_t(const void* q_idx, const void* k_cache, long long page_stride,
-                                const dsa::IndexPagedParams& p, bool pdl, cudaStream_t stream) {
+                                const dsa::IndexPagedParams& p, cudaStream_t stream) {
   using C = dsa::IndexPagedCfg<H_I, D_I>;
   auto kern = dsa::index_paged_kernel<H_I, D_I>;
   static DeviceFlag attr_done;
@@ -378,16 +378,16 @@ static int index_paged_launch_t(const void* q_idx, const void* k_cache, long lon
   if (st != DSA_OK) return st;
   const long long tiles = (long long)p.batch * ((p.max_len + 127) / 128);
   const long long grid = std::max<long long>(1, std::min<long long>(tiles, sm_count()));
-  return launch_pdl(pdl, kern, dim3((unsigned)grid), dim3(C::THREADS), (size_t)smem, stream, tk, tq, p);
+  return launch_pdl(true, kern, dim3((unsigned)grid), dim3(C::THREADS), (size_t)smem, stream, tk, tq, p);
 }
 
 int index_paged_launch(const void* q_idx, const void* k_cache, long long page_stride, const dsa::IndexPagedParams& p,
-                       int H_I, int d_I, bool pdl, cudaStream_t stream) {
-  if (H_I == 64 && d_I == 128) return index_paged_launch_t<64, 128>(q_idx, k_cache, page_stride, p, pdl, stream);
-  if (H_I == 32 && d_I == 128) return index_paged_launch_t<32, 128>(q_idx, k_cache, page_stride, p, pdl, stream);
-  if (H_I == 16 && d_I == 128) return index_paged_launch_t<16, 128>(q_idx, k_cache, page_stride, p, pdl, stream);
-  if (H_I == 8 && d_I == 64) return index_paged_launch_t<8, 64>(q_idx, k_cache, page_stride, p, pdl, stream);
-  if (H_I == 4 && d_I == 32) return index_paged_launch_t<4, 32>(q_idx, k_cache, page_stride, p, pdl, stream);
+                       int H_I, int d_I, cudaStream_t stream) {
+  if (H_I == 64 && d_I == 128) return index_paged_launch_t<64, 128>(q_idx, k_cache, page_stride, p, stream);
+  if (H_I == 32 && d_I == 128) return index_paged_launch_t<32, 128>(q_idx, k_cache, page_stride, p, stream);
+  if (H_I == 16 && d_I == 128) return index_paged_launch_t<16, 128>(q_idx, k_cache, page_stride, p, stream);
+  if (H_I == 8 && d_I == 64) return index_paged_launch_t<8, 64>(q_idx, k_cache, page_stride, p, stream);
+  if (H_I == 4 && d_I == 32) return index_paged_launch_t<4, 32>(q_idx, k_cache, page_stride, p, stream);
   return DSA_ERR_UNSUPPORTED;
 }
 

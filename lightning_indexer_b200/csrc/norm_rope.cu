@@ -765,7 +765,7 @@ static int plan_segs(dsa::HeadRowsParams& p, int run, bool whole, long long tota
 }
 
 template <bool ZERO>
-static int head_rows_fwd_kernel_launch(const dsa::HeadRowsParams& p, int d, int inter, int blocks, bool pdl, cudaStream_t stream) {
+static int head_rows_fwd_kernel_launch(const dsa::HeadRowsParams& p, int d, int inter, int blocks, cudaStream_t stream) {
   auto kern = d == 128 && inter ? dsa::head_rows_fwd_kernel<128, 1, ZERO>
               : d == 128        ? dsa::head_rows_fwd_kernel<128, 0, ZERO>
               : d == 64 && inter ? dsa::head_rows_fwd_kernel<64, 1, ZERO>
@@ -773,7 +773,7 @@ static int head_rows_fwd_kernel_launch(const dsa::HeadRowsParams& p, int d, int 
               : d == 32 && inter ? dsa::head_rows_fwd_kernel<32, 1, ZERO>
               : d == 32          ? dsa::head_rows_fwd_kernel<32, 0, ZERO>
                                  : dsa::head_rows_fwd_kernel<0, -1, false>;
-  return launch_pdl(pdl, kern, dim3((unsigned)blocks), dim3(dsa::NR_FWD_WARPS * 32), 0, stream, p);
+  return launch_pdl(true, kern, dim3((unsigned)blocks), dim3(dsa::NR_FWD_WARPS * 32), 0, stream, p);
 }
 
 // Forward: a warp for every run.  Blocks that come and go balance rows of different cost: at
@@ -782,7 +782,7 @@ static int head_rows_fwd_kernel_launch(const dsa::HeadRowsParams& p, int d, int 
 // Runs of 8 groups (4: 112 us, 12: 98), fewer where the rows do not fill the SMs otherwise; past
 // one and a half waves whole tokens, whose turns are then computed once (1024 tokens: 5.8 us,
 // 7.8 without).
-int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) {
+int head_rows_fwd_launch(dsa::HeadRowsParams& p, cudaStream_t stream) {
   long long groups = 0;
   for (int i = 0; i < p.nseg; ++i) groups += seg_groups(p, p.seg[i]);
   const long long wave = 20LL * sm_count();  // resident warps
@@ -795,9 +795,9 @@ int head_rows_fwd_launch(dsa::HeadRowsParams& p, bool pdl, cudaStream_t stream) 
   if (p.zero_outside) {  // (Q and K of one call agree)
     p.zero_block0 = blocks;
     blocks += std::min(blocks, sm_count());
-    return head_rows_fwd_kernel_launch<true>(p, d, inter, blocks, pdl, stream);
+    return head_rows_fwd_kernel_launch<true>(p, d, inter, blocks, stream);
   }
-  return head_rows_fwd_kernel_launch<false>(p, d, inter, blocks, pdl, stream);
+  return head_rows_fwd_kernel_launch<false>(p, d, inter, blocks, stream);
 }
 
 // Blocks of the backward: one wave, two blocks on each of a B200's SMs, since each block adds a

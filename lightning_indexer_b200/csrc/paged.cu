@@ -83,7 +83,7 @@ static int norm_rope_call(const void* Q, int64_t q_stride, const void* K, int64_
   // K's few heads per token cost more per row: they go first
   if (K) p.seg[p.nseg++] = head_seg(K, k_stride, k_weight, inv_freq, rotary_dim, interleaved, Hk, d, K_out, k_out_stride);
   p.seg[p.nseg++] = head_seg(Q, q_stride, q_weight, inv_freq, rotary_dim, interleaved, Hq, d, Q_out, q_out_stride);
-  return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
+  return head_rows_fwd_launch(p, static_cast<cudaStream_t>(stream));
 }
 
 static int norm_rope_bwd_call(const void* Q, int64_t q_stride, const void* K, int64_t k_stride, const void* dQ_out,
@@ -209,7 +209,7 @@ static int index_paged_args_status(const void* q_idx, const void* k_cache, int64
 static int index_paged_call(const void* q_idx, const void* k_cache, int64_t page_stride, const void* w,
                             const int32_t* table, int max_pages, const int32_t* lens, int batch, int num_pages,
                             int page_size, int max_seqlen_k, int H_I, int d_I, float* scores, int64_t ld, int* cu_q,
-                            int* cu_k, bool pdl, cudaStream_t stream) {
+                            int* cu_k, cudaStream_t stream) {
   const int st = index_paged_args_status(q_idx, k_cache, page_stride, w, table, max_pages, lens, batch, num_pages,
                                          page_size, max_seqlen_k, H_I, d_I);
   if (st == DSA_ERR_INVALID_ARG) return st;
@@ -228,7 +228,7 @@ static int index_paged_call(const void* q_idx, const void* k_cache, int64_t page
   p.ld = ld;
   p.cu_q = cu_q;
   p.cu_k = cu_k;
-  return index_paged_launch(q_idx, k_cache, page_stride, p, H_I, d_I, pdl, stream);
+  return index_paged_launch(q_idx, k_cache, page_stride, p, H_I, d_I, stream);
 }
 
 static int sparse_attn_paged_args_status(const void* Q, const void* k_cache, int64_t k_page_stride, const void* v_cache,
@@ -250,7 +250,7 @@ static int sparse_attn_paged_args_status(const void* Q, const void* k_cache, int
 static int sparse_attn_paged_call(const void* Q, const void* k_cache, int64_t k_page_stride, const void* v_cache,
                                   int64_t v_page_stride, const int32_t* indices, const int32_t* table, int max_pages,
                                   const int32_t* lens, int batch, int num_pages, int page_size, int Hq, int Hkv, int d,
-                                  int k, float scale, void* O, float* lse, bool pdl, cudaStream_t stream) {
+                                  int k, float scale, void* O, float* lse, cudaStream_t stream) {
   if (const int st = sparse_attn_paged_args_status(Q, k_cache, k_page_stride, v_cache, v_page_stride, indices, table,
                                                    max_pages, lens, batch, num_pages, page_size, Hq, Hkv, d, k, scale,
                                                    O);
@@ -275,7 +275,7 @@ static int sparse_attn_paged_call(const void* Q, const void* k_cache, int64_t k_
   p.scale_log2 = scale * 1.4426950408889634f;
   p.O = static_cast<uint16_t*>(O);
   p.lse = lse;
-  return sparse_attn_paged_launch(p, batch, d, pdl, stream);
+  return sparse_attn_paged_launch(p, batch, d, stream);
 }
 
 // Scratch of the paged decode: the offsets that the top-k reads, the scores, its workspace.
@@ -315,7 +315,7 @@ static int decode_paged_run(const void* q_idx, const void* w, const void* Q, con
                             const void* v_cache, int64_t v_page_stride, const void* ki_cache, int64_t ki_page_stride,
                             const int32_t* table, int max_pages, const int32_t* lens, int batch, int num_pages,
                             int page_size, int max_seqlen_k, int Hq, int Hkv, int d, int H_I, int d_I, int k,
-                            float scale, int32_t* indices, void* O, float* lse, void* workspace, bool pdl,
+                            float scale, int32_t* indices, void* O, float* lse, void* workspace,
                             cudaStream_t stream) {
   const DecodePagedWs L = decode_paged_ws(batch, max_seqlen_k);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -323,13 +323,13 @@ static int decode_paged_run(const void* q_idx, const void* w, const void* Q, con
   int* cu_k = reinterpret_cast<int*>(ws + L.cu_k);
   float* scores = reinterpret_cast<float*>(ws + L.scores);
   int st = index_paged_call(q_idx, ki_cache, ki_page_stride, w, table, max_pages, lens, batch, num_pages, page_size,
-                            max_seqlen_k, H_I, d_I, scores, L.ld, cu_q, cu_k, pdl, stream);
+                            max_seqlen_k, H_I, d_I, scores, L.ld, cu_q, cu_k, stream);
   if (st != DSA_OK) return st;
   st = topk_launch(scores, L.ld, cu_q, cu_k, batch, 0, batch, k, indices, (int)L.ld, L.topk_bytes ? ws + L.topk : nullptr,
                    L.topk_bytes, stream);
   if (st != DSA_OK) return st;
   return sparse_attn_paged_call(Q, k_cache, k_page_stride, v_cache, v_page_stride, indices, table, max_pages, lens,
-                                batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, true, stream);
+                                batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, stream);
 }
 
 }  // namespace dsa_host
@@ -411,7 +411,7 @@ DSA_API int dsa_cache_append(const void* K, int64_t k_stride, const void* V, int
   paged_segs(p, K, k_stride, V, v_stride, k_idx, k_idx_stride, k_weight, k_idx_weight, inv_freq, rotary_dim, interleaved,
              idx_inv_freq, idx_rotary_dim, idx_interleaved, Hkv, d, d_I, k_cache, k_page_stride, v_cache, v_page_stride,
              k_idx_cache, k_idx_page_stride, block_table, max_pages, num_pages, page_size);
-  return head_rows_fwd_launch(p, true, static_cast<cudaStream_t>(stream));
+  return head_rows_fwd_launch(p, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t k_idx_page_stride, const void* w,
@@ -419,7 +419,7 @@ DSA_API int dsa_index_paged(const void* q_idx, const void* k_idx_cache, int64_t 
                             int num_pages, int page_size, int max_seqlen_k, int H_I, int d_I, float* scores,
                             int64_t ld_scores, void* stream) {
   return index_paged_call(q_idx, k_idx_cache, k_idx_page_stride, w, block_table, max_pages, seqlens_k, batch, num_pages,
-                          page_size, max_seqlen_k, H_I, d_I, scores, ld_scores, nullptr, nullptr, true,
+                          page_size, max_seqlen_k, H_I, d_I, scores, ld_scores, nullptr, nullptr,
                           static_cast<cudaStream_t>(stream));
 }
 
@@ -429,7 +429,7 @@ DSA_API int dsa_sparse_attn_decode_paged(const void* Q, const void* k_cache, int
                                          int batch, int num_pages, int page_size, int Hq, int Hkv, int d, int k,
                                          float scale, void* O, float* lse, void* stream) {
   return sparse_attn_paged_call(Q, k_cache, k_page_stride, v_cache, v_page_stride, indices, block_table, max_pages,
-                                seqlens_k, batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse, true,
+                                seqlens_k, batch, num_pages, page_size, Hq, Hkv, d, k, scale, O, lse,
                                 static_cast<cudaStream_t>(stream));
 }
 
@@ -454,7 +454,7 @@ DSA_API int dsa_decode_paged(const void* q_idx, const void* w, const void* Q, co
     return DSA_ERR_WORKSPACE;
   return decode_paged_run(q_idx, w, Q, k_cache, k_page_stride, v_cache, v_page_stride, k_idx_cache, k_idx_page_stride,
                           block_table, max_pages, seqlens_k, batch, num_pages, page_size, max_seqlen_k, Hq, Hkv, d, H_I,
-                          d_I, k, scale, indices, O, lse, workspace, true, static_cast<cudaStream_t>(stream));
+                          d_I, k, scale, indices, O, lse, workspace, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API size_t dsa_decode_step_paged_workspace_size(int batch, int max_seqlen_k, int Hq, int d, int H_I, int d_I) {
@@ -508,10 +508,10 @@ DSA_API int dsa_decode_step_paged(const void* q_idx, int64_t q_idx_stride, const
              idx_inv_freq, idx_rotary_dim, idx_interleaved, Hkv, d, d_I, k_cache, k_page_stride, v_cache, v_page_stride,
              k_idx_cache, k_idx_page_stride, block_table, max_pages, num_pages, page_size);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (st = head_rows_fwd_launch(p, true, s); st != DSA_OK) return st;
+  if (st = head_rows_fwd_launch(p, s); st != DSA_OK) return st;
   return decode_paged_run(qi_out, w, q_out, k_cache, k_page_stride, v_cache, v_page_stride, k_idx_cache,
                           k_idx_page_stride, block_table, max_pages, seqlens_k, batch, num_pages, page_size,
-                          max_seqlen_k, Hq, Hkv, d, H_I, d_I, k, scale, indices, O, lse, ws, true, s);
+                          max_seqlen_k, Hq, Hkv, d, H_I, d_I, k, scale, indices, O, lse, ws, s);
 }
 
 }  // extern "C"

@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(WARPS * 32) sparse_attn_paged_kernel(const SAP
 namespace dsa_host {
 
 template <int D, int WARPS, bool SAME>
-static int sa_paged_launch_same(const dsa::SAPagedParams& p, long long groups, int splits, bool pdl, cudaStream_t stream) {
+static int sa_paged_launch_same(const dsa::SAPagedParams& p, long long groups, int splits, cudaStream_t stream) {
   constexpr int STAGES = 2;
   auto kern = dsa::sparse_attn_paged_kernel<D, WARPS, STAGES, SAME>;
   const int smem = dsa::SAPagedSmem<D, WARPS, STAGES>::BYTES;
@@ -398,10 +398,8 @@ static int sa_paged_launch_same(const dsa::SAPagedParams& p, long long groups, i
     attr[n].val.clusterDim.y = 1;
     attr[n++].val.clusterDim.z = 1;
   }
-  if (pdl) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = n;
   if (const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, splits); e != cudaSuccess) return cuda_fail(e);
@@ -409,9 +407,9 @@ static int sa_paged_launch_same(const dsa::SAPagedParams& p, long long groups, i
 }
 
 template <int D, int WARPS>
-static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int splits, bool pdl, cudaStream_t stream) {
-  return p.k_page_stride == p.v_page_stride ? sa_paged_launch_same<D, WARPS, true>(p, groups, splits, pdl, stream)
-                                            : sa_paged_launch_same<D, WARPS, false>(p, groups, splits, pdl, stream);
+static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int splits, cudaStream_t stream) {
+  return p.k_page_stride == p.v_page_stride ? sa_paged_launch_same<D, WARPS, true>(p, groups, splits, stream)
+                                            : sa_paged_launch_same<D, WARPS, false>(p, groups, splits, stream);
 }
 
 // While the (row, KV head) groups do not fill the SMs: blocks of 8 warps, one per SM, in the
@@ -422,21 +420,21 @@ static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int 
 // of 4 blocks of 4 warps, 22 and more as clusters of 8; 7 of 512 slots 6.1 us with 4 warps, 7.1
 // with 8; 64 of 2048 47 us unsplit with 4 warps, 50 with 8, 54 and more as clusters.
 template <int D>
-static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, bool pdl, cudaStream_t stream) {
+static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, cudaStream_t stream) {
   const long long groups = (long long)batch * p.Hkv, sms = sm_count();
-  if (groups > sms) return sa_paged_launch_t<D, 4>(p, groups, 1, pdl, stream);
+  if (groups > sms) return sa_paged_launch_t<D, 4>(p, groups, 1, stream);
   const int units = (p.k + 31) / 32;
   auto splits = [&](int warps) {
     int n = 1;
     while (n < dsa::SAP_MAX_SPLITS && groups * n * 2 <= sms && n * 2 * warps <= units) n *= 2;
     return n;
   };
-  if (splits(4) * 4 >= units) return sa_paged_launch_t<D, 4>(p, groups, splits(4), pdl, stream);
-  return sa_paged_launch_t<D, 8>(p, groups, splits(8), pdl, stream);
+  if (splits(4) * 4 >= units) return sa_paged_launch_t<D, 4>(p, groups, splits(4), stream);
+  return sa_paged_launch_t<D, 8>(p, groups, splits(8), stream);
 }
 
-int sparse_attn_paged_launch(const dsa::SAPagedParams& p, int batch, int d, bool pdl, cudaStream_t stream) {
-  return d == 128 ? sa_paged_launch_d<128>(p, batch, pdl, stream) : sa_paged_launch_d<64>(p, batch, pdl, stream);
+int sparse_attn_paged_launch(const dsa::SAPagedParams& p, int batch, int d, cudaStream_t stream) {
+  return d == 128 ? sa_paged_launch_d<128>(p, batch, stream) : sa_paged_launch_d<64>(p, batch, stream);
 }
 
 }  // namespace dsa_host
