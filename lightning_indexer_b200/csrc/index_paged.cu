@@ -16,8 +16,8 @@
 //     (each CTA sums the tile counts itself, there is no planning launch); a CTA walks its
 //     piece of the list and reloads the query where it crosses into the next sequence.
 //
-// Measured: 16 sequences of 262144 positions, 1 GiB of keys, in 172 to 177 us (6.2 TB/s); 64
-// ragged ones up to 16384 in 32.5 us (5.2 TB/s), of which 2.4 us pass before the first load
+// Measured: 16 sequences of 262144 positions, 1 GiB of keys, in 172 to 180 us (6.2 TB/s); 64
+// ragged ones up to 16384 in 32.6 us, 33.5 launched eagerly (5.1 TB/s), of which 2.4 us pass before the first load
 // (lengths, then the list, then the pages) and 1 after the last.
 #include <algorithm>
 

@@ -21,11 +21,14 @@
 // run's tokens (sequence, position, page) are looked up by its lanes side by side, one chain
 // of dependent loads per run instead of one per group.
 //
-// Bound by HBM (4 bytes an element forward, 6 backward) with the issue slots close behind:
-// about 210 instructions a group of 1 KiB forward, 300 backward.  Measured: 32768 tokens of
-// 32 + 4 heads of 128 in 96 to 103 us (6.2 to 5.9 TB/s), the backward of 65536 in 303 to 320 us
-// (6.0 to 5.7 TB/s), an append of 32768 tokens (4 + 4 heads and the indexer's key) in 30 us
-// (5.0 TB/s: every group of K is another token, whose turns it computes for itself).
+// Bound by HBM (4 bytes an element forward, 6 backward), with about 210 instructions a group of
+// 1 KiB forward, 300 backward (63 and 58 % of the issue slots).  Measured: 32768 tokens of
+// 32 + 4 heads of 128 in 95 to 103 us (6.3 to 5.9 TB/s), the backward of 65536 in 303 to 320 us
+// (6.0 to 5.7 TB/s; 128 registers a thread, of which the <128, 0> form spills 28 bytes), an append
+// of 32768 tokens (4 + 4 heads and the indexer's key) in 30 us (5.0 TB/s: every group of K is
+// another token, whose turns it computes for itself; its 2304 blocks are 3.1 waves).  The form for
+// tensors that do not agree in width or pairing spills 68 bytes: the same append takes 30.3 us
+// with interleaved pairs where it takes 29.2 without, and 22.6 at d = 64 with d_I = 128 (floor 12.8).
 #include <algorithm>
 
 #include "common.cuh"
@@ -66,7 +69,7 @@ struct TokenMap {
 };
 
 constexpr int NR_MAX_SEGS = 5;
-constexpr int NR_FWD_WARPS = 4;  // warps of a block; 5 blocks per SM at 102 registers (8 x 3 spills, 8 x 2 waits)
+constexpr int NR_FWD_WARPS = 4;  // warps of a block; 5 blocks per SM: at most 102 registers (8 x 3 spills, 8 x 2 waits)
 constexpr int NR_BWD_WARPS = 8;  // 2 blocks per SM
 constexpr int NR_BWD_BLOCKS = 2 * 148;
 

@@ -15,10 +15,11 @@
 // output to the block that finishes it (remote stores, one barrier, local sums), always summed
 // in the same order.
 //
-// Measured: 16 sequences, 2048 of 262144 positions each (67 MB), in 17.3 us: 2.6 us until the
-// first copy starts (position, then its page, then its row), 10 us of streaming at 6.0 TB/s,
-// 2 us to join the states; 64 sequences (270 MB) in 47 us.  Halving the instructions of the
-// gather changed nothing; more stages, or more warps per SM, neither.
+// Measured: 16 sequences, 2048 of 262144 positions each (67 MB), in 17.4 us, 17.8 launched
+// eagerly: 2.6 us until the first copy starts (position, then its page, then its row), 10 us of
+// streaming at 6.0 TB/s, 2 us to join the states; its 128 blocks leave 20 of the 148 SMs idle.  64
+// sequences (270 MB) in 62 us, 54 where each has 8192 positions.  Halving the instructions of
+// the gather changed nothing; more stages, or more warps per SM, neither.
 #include <algorithm>
 #include <cooperative_groups.h>
 #include <type_traits>
@@ -416,9 +417,11 @@ static int sa_paged_launch_t(const dsa::SAPagedParams& p, long long groups, int 
 // largest cluster that still gives every block an SM of its own and every warp a unit, or of 4
 // warps where those already give every unit its warp.  Past that, blocks of 4 warps, three per
 // SM, without clusters.  Joining over a cluster costs about 1.5 us, so more and smaller pieces
-// lose: 16 sequences of 2048 slots (64 groups) take 17.0 us as clusters of 2, 17.5 as clusters
-// of 4 blocks of 4 warps, 22 and more as clusters of 8; 7 of 512 slots 6.1 us with 4 warps, 7.1
-// with 8; 64 of 2048 47 us unsplit with 4 warps, 50 with 8, 54 and more as clusters.
+// lose: 16 sequences of 2048 slots (64 groups) take 17.4 us as clusters of 2 blocks of 8 warps,
+// 21.3 and 22.1 as clusters of 2 and 4 blocks of 4, 22.6 without clusters; 7 of 512 slots 6.2 us as
+// clusters of 4 blocks of 4, 6.6 as clusters of 2 of 8.  Past one wave the two widths are close
+// and neither always wins: 64 sequences of 2048 slots took 47 us with 4 warps and 50 with 8 when
+// the rule was set, 62 and 52 later, from contexts of 262144 positions.
 template <int D>
 static int sa_paged_launch_d(const dsa::SAPagedParams& p, int batch, cudaStream_t stream) {
   const long long groups = (long long)batch * p.Hkv, sms = sm_count();
